@@ -60,6 +60,8 @@ extern "C" {
  * [G][N][K/2] (moe_quant_weight_mx with MOE_MX_E2M1) with the same tiled MX
  * scales. */
 #define MOE_DTYPE_FP8_MXFP4 3
+/* fp32 tensors of the training calls (weight gradients, parameters). */
+#define MOE_DTYPE_FP32 16
 
 /* device error word bits (see moe_get_device_error) */
 #define MOE_DEVERR_MASKED_OVERFLOW 1  /* an expert received more than max_m rows */
@@ -381,6 +383,144 @@ int32_t moe_combine(const void* Y, int64_t num_rows, const int32_t* src2dst,
                     const float* topk_weights, int32_t T, int32_t k, int32_t H, void* out,
                     void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Training: gradients of the calls above and the AdamW step.  All BF16 (weights
+ * held in FP8 or MX formats have no gradient here).  Device pointers of tensors
+ * must be 16-byte aligned -> else MOE_EUNSUPPORTED.  Every gradient is the same
+ * from run to run: no sum depends on the order in which workgroups finish.
+ * ------------------------------------------------------------------------- */
+
+/* Gradient of moe_combine.  For every slot with r = src2dst[t][j] in
+ * [0, num_rows):
+ *   dY[r][h] = topk_weights[t][j] * dout[t][h]            (rounded to bf16)
+ *   dtopk_weights[t][j] = sum over h of dout[t][h] * Y[r][h]  (fp32)
+ * and dtopk_weights[t][j] = 0 for the other slots.  Serves both layouts.
+ *   dout bf16 [T][H]; Y, dY bf16 [num_rows][H]; src2dst int32 [T][k];
+ *   topk_weights, dtopk_weights fp32 [T][k].
+ *   Rows of dY that no slot names (padding) are left as they were.  The rows
+ *   named must be distinct (as the scatter leaves them); a row named twice gets
+ *   one of its two values.  dY must not overlap the inputs.
+ * Limits: H % 8 == 0, 1 <= k <= 32. */
+int32_t moe_combine_bwd(const void* dout, const void* Y, int64_t num_rows, const int32_t* src2dst,
+                        const float* topk_weights, int32_t T, int32_t k, int32_t H, void* dY,
+                        float* dtopk_weights, void* stream);
+
+/* Gradient of moe_route_topk: the weights are the softmax of the kept logits, so
+ *   dlogits[t][topk_ids[t][j]] = w_j * (dw_j - sum over i of w_i * dw_i)
+ * with w = topk_weights[t], dw = dtopk_weights[t], and 0 for every other expert
+ * (all fp32; an id named twice gets the sum of its terms, ids outside [0, E)
+ * are skipped).  Linear in dw: where the experts are shared out, the shares'
+ * results add up to the whole gradient.
+ *   dlogits fp32 [T][E].  Limits as moe_route_topk. */
+int32_t moe_route_topk_bwd(const int32_t* topk_ids, const float* topk_weights,
+                           const float* dtopk_weights, int32_t T, int32_t E, int32_t k,
+                           float* dlogits, void* stream);
+
+/* Gradient of the scatter: dx[t][h] = sum over j with src2dst[t][j] in
+ * [0, num_rows) of dX[src2dst[t][j]][h], added in fp32 in slot order and
+ * rounded once to bf16; 0 for a token without such a slot.  Serves both layouts.
+ *   dX bf16 [num_rows][H]; dx bf16 [T][H].
+ * Limits: H % 8 == 0, 1 <= k <= 32. */
+int32_t moe_scatter_bwd(const void* dX, int64_t num_rows, const int32_t* src2dst, int32_t T,
+                        int32_t k, int32_t H, void* dx, void* stream);
+
+/* Gradient of silu_and_mul (bf16 output).  With g, u the halves of a row and
+ * s = 1 / (1 + e^-g), in fp32:
+ *   dgateup[r][i] = dact * u * s * (1 + g * (1 - s)),  dgateup[r][I+i] = dact * g * s,
+ *   act[r][i] = silu(g) * u  (only if act is not NULL: the forward's activation
+ *   again, bit for bit),
+ * each rounded once to bf16.  Rows are chosen as in silu_and_mul; skipped rows
+ * are left as they were.
+ *   gateup, dgateup bf16 [M][2I] (may be one buffer); dact, act bf16 [M][I].
+ * Limits: I % 128 == 0, I <= 67107840. */
+int32_t silu_and_mul_bwd(const void* gateup, const void* dact, int64_t M, int32_t I,
+                         const int32_t* m_indices, const int32_t* masked_m, int32_t max_m,
+                         void* dgateup, void* act, void* stream);
+
+/* Gradient of grouped_gemm_contig with respect to A:
+ *   dA[r][:] = dC[r][:] . B[m_indices[r]]   (the sum runs over N, in fp32)
+ * rounded to bf16.
+ *   dC bf16 [M][N]; B bf16 [G][N][K]; dA bf16 [M][K]; m_indices as
+ *   grouped_gemm_contig.  Rows with m_indices < 0 are left as they were.
+ *   A row's result depends on its own dC row and its expert's weights alone.
+ * Limits: N % 128 == 0, K % 128 == 0, N, K <= 4194304, G <= 1024,
+ * ceil(M / 128) <= 8176 -> else MOE_EUNSUPPORTED. */
+int32_t grouped_gemm_contig_dgrad(const void* dC, const void* B, void* dA,
+                                  const int32_t* m_indices, int64_t M, int32_t N, int32_t K,
+                                  int32_t G, void* stream);
+
+/* Gradient of grouped_gemm_contig with respect to B:
+ *   dB[g][n][k] = sum over r in [expert_start_loc[g], expert_start_loc[g] +
+ *   num_valid[g]) of dC[r][n] * A[r][k]   (fp32), added to what dB holds if
+ * accumulate is not 0, and rounded once to dB's type.  Experts without rows get
+ * 0 (or keep what they hold).  Rows outside the experts' ranges are not part of
+ * any sum, whatever they hold; ranges are cut at M.
+ *   dC bf16 [M][N]; A bf16 [M][K]; dB [G][N][K], out_dtype MOE_DTYPE_BF16 or
+ *   MOE_DTYPE_FP32; expert_start_loc, num_valid as moe_scatter_compact writes
+ *   them.
+ * Limits as grouped_gemm_contig_dgrad. */
+int32_t grouped_gemm_contig_wgrad(const void* dC, const void* A, const int32_t* expert_start_loc,
+                                  const int32_t* num_valid, int32_t out_dtype, int32_t accumulate,
+                                  void* dB, int64_t M, int32_t N, int32_t K, int32_t G,
+                                  void* stream);
+
+/* One tensor of an AdamW step.
+ *   param         device bf16 or fp32 [numel] (param_dtype MOE_DTYPE_BF16 or
+ *                 MOE_DTYPE_FP32)
+ *   master        device fp32 [numel]: the weight itself where param is bf16
+ *                 (param is its rounding); NULL where param is fp32
+ *   grad          device bf16 or fp32 [numel] (grad_dtype)
+ *   m, v          state_bits 32: device fp32 [numel], the running means of the
+ *                 gradient and of its square.  state_bits 8: device u8, numel
+ *                 rounded up to 128: the e4m3 codes of m and of the root of v
+ *   m_scale, v_scale  state_bits 8: device u8 [ceil(numel / 128)], the UE8M0
+ *                 scale of each 128 elements; else NULL
+ *   weight_decay  of this tensor */
+typedef struct {
+  void* param;
+  float* master;
+  const void* grad;
+  void* m;
+  void* v;
+  uint8_t* m_scale;
+  uint8_t* v_scale;
+  int64_t numel;
+  float weight_decay;
+  int32_t param_dtype;
+  int32_t grad_dtype;
+  int32_t state_bits;
+} moe_adamw_tensor;
+
+/* Host: bytes of the plan for n tensors, 0 where they are invalid. */
+size_t moe_adamw_plan_bytes(const moe_adamw_tensor* tensors, int32_t n);
+
+/* Host: writes the plan of n tensors to host_plan.  The caller copies its
+ * plan_bytes bytes to the device once and keeps them there for as long as the
+ * tensors stay where they are.  Fewer than moe_adamw_plan_bytes -> MOE_ECAPACITY. */
+int32_t moe_adamw_plan(const moe_adamw_tensor* tensors, int32_t n, void* host_plan,
+                       size_t plan_bytes);
+
+/* One AdamW step over the plan's tensors, in one launch.  With t = counter[0] + 1
+ * and g the gradient times *grad_scale, in fp32:
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
+ *   w = w (1 - lr wd) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * (1 - beta^t in double).  The step uses m and v before they are rounded to 8
+ * bits.  8-bit states: for each 128 elements e is the smallest integer in
+ * [-126, 127] with amax <= 448 * 2^e; x * 2^-e is cut to e4m3 after adding 16
+ * random bits below its last place (so its expectation is x; a positive root of
+ * v never becomes 0).  The bits are a hash of (seed, t, tensor's place in the
+ * plan, element): the same call on the same state gives the same result.
+ *   plan       device copy of the plan, plan_bytes its size, 16-byte aligned
+ *   lr         device fp32 [1], grad_scale device fp32 [1] or NULL (1): read by
+ *              the kernel, so a captured step follows them
+ *   counter    device int64 [2]: the number of steps taken (>= 0), and 0.  The
+ *              call counts its step; two steps on one counter must not overlap
+ * Non-finite gradients make their weight NaN and leave their group's 8-bit
+ * states unspecified.
+ * Limits: 0 <= beta < 1, eps > 0 -> else MOE_EINVAL. */
+int32_t moe_adamw_step(const void* plan, size_t plan_bytes, const float* lr,
+                       const float* grad_scale, int64_t* counter, double beta1, double beta2,
+                       float eps, uint32_t seed, void* stream);
 
 #ifdef __cplusplus
 }

@@ -18,6 +18,7 @@ _lib = None
 
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_ECAPACITY, MOE_EDEVICE = 0, 1, 2, 3, 4
 MOE_DTYPE_BF16, MOE_DTYPE_FP8_E4M3_UE8M0, MOE_DTYPE_FP8_E4M3_MXFP8, MOE_DTYPE_FP8_MXFP4 = 0, 1, 2, 3
+MOE_DTYPE_FP32 = 16
 MOE_MX_E4M3, MOE_MX_E2M1 = 0, 1
 MOE_DEVERR_MASKED_OVERFLOW = 1
 MOE_SCATTER_NOALLOC_MAX_BYTES = 4 << 20
@@ -52,7 +53,24 @@ SIGNATURES = {
                                         _I32, _I32, _P]),
     "silu_and_mul": (_I32, [_P, _I64, _I32, _P, _P, _I32, _I32, _P, _P, _P]),
     "moe_combine": (_I32, [_P, _I64, _P, _P, _I32, _I32, _I32, _P, _P]),
+    "moe_combine_bwd": (_I32, [_P, _P, _I64, _P, _P, _I32, _I32, _I32, _P, _P, _P]),
+    "moe_route_topk_bwd": (_I32, [_P, _P, _P, _I32, _I32, _I32, _P, _P]),
+    "moe_scatter_bwd": (_I32, [_P, _I64, _P, _I32, _I32, _I32, _P, _P]),
+    "silu_and_mul_bwd": (_I32, [_P, _P, _I64, _I32, _P, _P, _I32, _P, _P, _P]),
+    "grouped_gemm_contig_dgrad": (_I32, [_P, _P, _P, _P, _I64, _I32, _I32, _I32, _P]),
+    "grouped_gemm_contig_wgrad": (_I32, [_P, _P, _P, _P, _I32, _I32, _P, _I64, _I32, _I32, _I32, _P]),
+    "moe_adamw_plan_bytes": (_SZ, [_P, _I32]),
+    "moe_adamw_plan": (_I32, [_P, _I32, _P, _SZ]),
+    "moe_adamw_step": (_I32, [_P, _SZ, _P, _P, _P, ctypes.c_double, ctypes.c_double, ctypes.c_float,
+                              ctypes.c_uint32, _P]),
 }
+
+
+class AdamwTensor(ctypes.Structure):
+    """moe_adamw_tensor of include/moe.h."""
+    _fields_ = [("param", _P), ("master", _P), ("grad", _P), ("m", _P), ("v", _P), ("m_scale", _P),
+                ("v_scale", _P), ("numel", _I64), ("weight_decay", ctypes.c_float),
+                ("param_dtype", _I32), ("grad_dtype", _I32), ("state_bits", _I32)]
 
 
 class MoeError(RuntimeError):
@@ -310,3 +328,120 @@ def moe_combine(Y, src2dst, topk_weights, out):
     rows = Y.numel() // H
     _check("moe_combine", lib().moe_combine(_ptr(Y), rows, _ptr(src2dst), _ptr(topk_weights), T, k,
                                             H, _ptr(out), _stream()))
+
+
+# --- training: gradients and the optimizer step -------------------------------------
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _dev(name: str, dtype, shape, t) -> int:
+    """Data pointer of an operand of the training calls: a contiguous tensor of
+    this dtype and shape on the current device (the stream's)."""
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name}: want {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: is on {t.device}, not on the current device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+_BF16, _F32, _INT32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def moe_combine_bwd(dout, Y, src2dst, topk_weights, dY, dtopk_weights):
+    """Gradient of moe_combine: dY [rows, H] (rows that no slot names keep what
+    they hold) and dtopk_weights [T, k]."""
+    _need(dout.dim() == 2 and src2dst.dim() == 2, "moe_combine_bwd: dout and src2dst are matrices")
+    T, H = dout.shape
+    k = src2dst.shape[1]
+    _need(Y.shape[-1] == H, "moe_combine_bwd: Y and dout differ in width")
+    rows = Y.numel() // H if H else 0
+    _check("moe_combine_bwd", lib().moe_combine_bwd(
+        _dev("dout", _BF16, (T, H), dout), _dev("Y", _BF16, Y.shape, Y), rows,
+        _dev("src2dst", _INT32, (T, k), src2dst), _dev("topk_weights", _F32, (T, k), topk_weights), T, k, H,
+        _dev("dY", _BF16, Y.shape, dY), _dev("dtopk_weights", _F32, (T, k), dtopk_weights), _stream()))
+
+
+def moe_route_topk_bwd(topk_ids, topk_weights, dtopk_weights, dlogits):
+    """Gradient of moe_route_topk: dlogits [T, E], zero outside the kept experts."""
+    _need(topk_ids.dim() == 2 and dlogits.dim() == 2, "moe_route_topk_bwd: topk_ids and dlogits are matrices")
+    T, k = topk_ids.shape
+    E = dlogits.shape[1]
+    _check("moe_route_topk_bwd", lib().moe_route_topk_bwd(
+        _dev("topk_ids", _INT32, (T, k), topk_ids), _dev("topk_weights", _F32, (T, k), topk_weights),
+        _dev("dtopk_weights", _F32, (T, k), dtopk_weights), T, E, k,
+        _dev("dlogits", _F32, (T, E), dlogits), _stream()))
+
+
+def moe_scatter_bwd(dX, src2dst, dx):
+    """Gradient of the scatter: dx [T, H], the sum of a token's gradient rows."""
+    _need(src2dst.dim() == 2 and dx.dim() == 2, "moe_scatter_bwd: src2dst and dx are matrices")
+    T, k = src2dst.shape
+    H = dx.shape[1]
+    _need(dX.shape[-1] == H, "moe_scatter_bwd: dX and dx differ in width")
+    rows = dX.numel() // H if H else 0
+    _check("moe_scatter_bwd", lib().moe_scatter_bwd(
+        _dev("dX", _BF16, dX.shape, dX), rows, _dev("src2dst", _INT32, (T, k), src2dst), T, k, H,
+        _dev("dx", _BF16, (T, H), dx), _stream()))
+
+
+def silu_and_mul_bwd(gateup, dact, dgateup, act=None, m_indices=None, masked_m=None, max_m=0):
+    """Gradient of silu_and_mul: dgateup [M, 2I] (may be gateup itself) and, if
+    given, the activation act [M, I] again."""
+    _need(gateup.dim() == 2 and gateup.shape[1] % 2 == 0, "silu_and_mul_bwd: gateup is [M, 2I]")
+    M, N = gateup.shape
+    I = N // 2
+    _need(masked_m is None or (max_m > 0 and masked_m.numel() * max_m == M),
+          "silu_and_mul_bwd: masked_m and max_m do not make up M rows")
+    _check("silu_and_mul_bwd", lib().silu_and_mul_bwd(
+        _dev("gateup", _BF16, (M, N), gateup), _dev("dact", _BF16, (M, I), dact), M, I,
+        None if m_indices is None else _dev("m_indices", _INT32, (M,), m_indices),
+        None if masked_m is None else _dev("masked_m", _INT32, masked_m.shape, masked_m), max_m,
+        _dev("dgateup", _BF16, (M, N), dgateup),
+        None if act is None else _dev("act", _BF16, (M, I), act), _stream()))
+
+
+def grouped_gemm_contig_dgrad(dC, B, dA, m_indices):
+    """Gradient of grouped_gemm_contig (bf16) with respect to A: dA [M, K] from
+    dC [M, N] and B [G, N, K]; rows with m_indices < 0 keep what they hold."""
+    _need(dC.dim() == 2 and B.dim() == 3, "grouped_gemm_contig_dgrad: dC is [M, N] and B [G, N, K]")
+    M = dC.shape[0]
+    G, N, K = B.shape
+    _check("grouped_gemm_contig_dgrad", lib().grouped_gemm_contig_dgrad(
+        _dev("dC", _BF16, (M, N), dC), _dev("B", _BF16, (G, N, K), B), _dev("dA", _BF16, (M, K), dA),
+        _dev("m_indices", _INT32, (M,), m_indices), M, N, K, G, _stream()))
+
+
+def grouped_gemm_contig_wgrad(dC, A, expert_start_loc, num_valid, dB, accumulate=False):
+    """Gradient of grouped_gemm_contig (bf16) with respect to B: dB [G, N, K] in
+    bf16 or fp32, replaced or (accumulate) added to."""
+    _need(dC.dim() == 2 and dB.dim() == 3, "grouped_gemm_contig_wgrad: dC is [M, N] and dB [G, N, K]")
+    M = dC.shape[0]
+    G, N, K = dB.shape
+    _need(dB.dtype in (_BF16, _F32), "grouped_gemm_contig_wgrad: dB is bf16 or fp32")
+    _check("grouped_gemm_contig_wgrad", lib().grouped_gemm_contig_wgrad(
+        _dev("dC", _BF16, (M, N), dC), _dev("A", _BF16, (M, K), A),
+        _dev("expert_start_loc", _INT32, (G,), expert_start_loc), _dev("num_valid", _INT32, (G,), num_valid),
+        MOE_DTYPE_FP32 if dB.dtype is _F32 else MOE_DTYPE_BF16, int(bool(accumulate)),
+        _dev("dB", dB.dtype, (G, N, K), dB), M, N, K, G, _stream()))
+
+
+def moe_adamw_plan(tensors) -> torch.Tensor:
+    """Host plan (uint8 tensor) of a list of AdamwTensor; copy it to the device."""
+    arr = (AdamwTensor * len(tensors))(*tensors)
+    n = lib().moe_adamw_plan_bytes(arr, len(tensors))
+    plan = torch.zeros(max(n, 16), dtype=torch.uint8)
+    _check("moe_adamw_plan", lib().moe_adamw_plan(arr, len(tensors), plan.data_ptr(), n))
+    return plan
+
+
+def moe_adamw_step(plan, lr, counter, beta1, beta2, eps, seed=0, grad_scale=None):
+    """One AdamW step over the tensors of a device plan."""
+    _check("moe_adamw_step", lib().moe_adamw_step(
+        _dev("plan", torch.uint8, plan.shape, plan), plan.numel(), _dev("lr", _F32, (1,), lr),
+        None if grad_scale is None else _dev("grad_scale", _F32, (1,), grad_scale),
+        _dev("counter", torch.int64, (2,), counter), beta1, beta2, eps, seed & 0xffffffff, _stream()))

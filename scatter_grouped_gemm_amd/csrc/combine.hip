@@ -5,13 +5,16 @@
 // summed in order j = 0..k-1 with explicit round-to-nearest fp32 multiply and
 // add (no contraction), so the result is the same for a token whatever batch
 // it arrives in.
+// The gradient of the scatter is the same sum without weights (each copy of a
+// token passes its gradient back unchanged), so it is the same kernel with
+// WEIGHTED false.
 #include "common.h"
 
 namespace moe {
 
 typedef __attribute__((ext_vector_type(4))) unsigned int u32x4_nt;
 
-template <int KMAX>
+template <int KMAX, bool WEIGHTED = true>
 __global__ __launch_bounds__(KMAX <= 8 ? 1024 : 256) void combine_kernel(const uint16_t* __restrict__ Y,
                                                       int64_t num_rows,
                                                       const int32_t* __restrict__ src2dst,
@@ -24,7 +27,7 @@ __global__ __launch_bounds__(KMAX <= 8 ? 1024 : 256) void combine_kernel(const u
   if (threadIdx.x < k) {
     const int r = src2dst[static_cast<int64_t>(t) * k + threadIdx.x];
     rows[threadIdx.x] = r < num_rows ? r : -1;
-    wt[threadIdx.x] = w[static_cast<int64_t>(t) * k + threadIdx.x];
+    if constexpr (WEIGHTED) wt[threadIdx.x] = w[static_cast<int64_t>(t) * k + threadIdx.x];
   }
   __syncthreads();
   for (int col = threadIdx.x * 8; col < H; col += blockDim.x * 8) {
@@ -46,7 +49,8 @@ __global__ __launch_bounds__(KMAX <= 8 ? 1024 : 256) void combine_kernel(const u
 #pragma unroll
     for (int j = 0; j < KMAX; ++j) {
       if (j >= k || rows[j] < 0) continue;
-      const float wj = wt[j];
+      float wj = 1.0f;
+      if constexpr (WEIGHTED) wj = wt[j];
       const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -85,6 +89,30 @@ extern "C" int32_t moe_combine(const void* Y, int64_t num_rows, const int32_t* s
     moe::combine_kernel<8><<<T, nt, 0, s>>>(y, num_rows, src2dst, topk_weights, k, H, o);
   else
     moe::combine_kernel<32><<<T, nt < 256 ? nt : 256, 0, s>>>(y, num_rows, src2dst, topk_weights, k, H, o);
+  MOE_CHECK_LAUNCH();
+  return MOE_OK;
+}
+
+extern "C" int32_t moe_scatter_bwd(const void* dX, int64_t num_rows, const int32_t* src2dst, int32_t T,
+                                   int32_t k, int32_t H, void* dx, void* stream) {
+  if (T < 0 || k < 1 || k > 32 || H <= 0 || num_rows < 0) return MOE_EINVAL;
+  if (H % 8 != 0) return MOE_EUNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!src2dst || !dx || (num_rows > 0 && !dX)) return MOE_EINVAL;
+  if ((reinterpret_cast<uintptr_t>(dX) | reinterpret_cast<uintptr_t>(dx)) & 15) return MOE_EUNSUPPORTED;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int need = (H / 8 + 63) / 64 * 64;
+  const int nt = need < 1024 ? need : 1024;
+  const uint16_t* y = static_cast<const uint16_t*>(dX);
+  uint16_t* o = static_cast<uint16_t*>(dx);
+  if (k <= 2)
+    moe::combine_kernel<2, false><<<T, nt, 0, s>>>(y, num_rows, src2dst, nullptr, k, H, o);
+  else if (k <= 4)
+    moe::combine_kernel<4, false><<<T, nt, 0, s>>>(y, num_rows, src2dst, nullptr, k, H, o);
+  else if (k <= 8)
+    moe::combine_kernel<8, false><<<T, nt, 0, s>>>(y, num_rows, src2dst, nullptr, k, H, o);
+  else
+    moe::combine_kernel<32, false><<<T, nt < 256 ? nt : 256, 0, s>>>(y, num_rows, src2dst, nullptr, k, H, o);
   MOE_CHECK_LAUNCH();
   return MOE_OK;
 }

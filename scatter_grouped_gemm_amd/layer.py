@@ -15,12 +15,19 @@ when there are non-local experts and at most 32 local ones).  The activation dty
 follows the weights ("[Feature] Support BF16 and batch-invariant inference
 with DeepEP v2", implementation breakdown item 2): FP8 weights make the path
 FP8, and asking for the other dtype is an error.
+
+Training (``train=True``, BF16 weights, compact layout): forward keeps what the
+gradients need in its own buffers and backward(dout) walks the same steps back --
+combine, w2 (weight, then input), SiLU-and-mul, w13 (weight, then input),
+scatter -- with no further host work; optimizer() gives the AdamW step over the
+expert weights.
 """
 from __future__ import annotations
 
 import torch
 
 from . import _lib as L
+from .optim import AdamW
 
 
 class MoELayer:
@@ -28,7 +35,8 @@ class MoELayer:
                  max_tokens: int, num_local_experts: int | None = None, expert_start: int = 0,
                  fp8: bool = False, layout: str = "auto", block_e: int = 128,
                  max_m: int | None = None, expected_m: int = 0, fuse_silu: bool = True,
-                 weight_format: str | None = None, device="cuda"):
+                 weight_format: str | None = None, train: bool = False,
+                 grad_dtype: torch.dtype = torch.bfloat16, device="cuda"):
         self.H, self.I, self.E, self.k = hidden, intermediate, num_experts, top_k
         self.El = num_local_experts or num_experts
         self.expert_start = expert_start
@@ -46,6 +54,16 @@ class MoELayer:
         self.block_e = block_e
         self.T_max = max_tokens
         self.device = torch.device(device)
+        self.train = train
+        if train:
+            if fp8:
+                raise ValueError("training needs BF16 weights: quantised weights have no gradient")
+            if layout not in ("auto", "compact"):
+                raise ValueError("training uses the compact layout")
+            if grad_dtype not in (torch.bfloat16, torch.float32):
+                raise ValueError(f"weight gradients are bf16 or fp32, not {grad_dtype}")
+            layout, fuse_silu = "compact", False     # backward needs the gate and up halves
+        self.grad_dtype = grad_dtype
         if layout == "auto":
             layout = "masked" if L.moe_choose_layout(max_tokens, top_k, self.E, self.El, block_e) else "compact"
         elif layout == "rule":
@@ -86,6 +104,13 @@ class MoELayer:
         ws_bytes = L.moe_scatter_ws_bytes(T, k, El, H)
         self.ws = torch.empty((ws_bytes + 3) // 4, dtype=torch.int32, device=d)
         self.w13 = self.w2 = self.w13_scale = self.w2_scale = None
+        if train:
+            self.dy = torch.empty(R, H, dtype=torch.bfloat16, device=d)
+            self.dx = torch.empty(T, H, dtype=torch.bfloat16, device=d)
+            self.dtopk_weights = torch.empty(T, k, dtype=torch.float32, device=d)
+            self.dlogits = torch.empty(T, self.E, dtype=torch.float32, device=d)
+        self.dw13 = self.dw2 = None
+        self._saved = None        # what the last forward left for backward
         # optional timing: name -> list of (start, end) HIP events recorded on
         # the current stream around each step of forward()
         self.marks = None
@@ -214,9 +239,71 @@ class MoELayer:
         out = self.out[:T]
         with self._mark("combine"):
             L.moe_combine(self.y, s2d, tw, out)
+        if self.train:
+            self._saved = (T, ids, tw, topk_ids is None)
         return out
 
     __call__ = forward
+
+    # -- training ---------------------------------------------------------------------
+
+    def allocate_grads(self):
+        """The weight gradients dw13 [El, 2I, H] and dw2 [El, H, I], zero."""
+        if not self.train:
+            raise ValueError("the layer was made without train=True")
+        self.dw13 = torch.zeros(self.El, 2 * self.I, self.H, dtype=self.grad_dtype, device=self.device)
+        self.dw2 = torch.zeros(self.El, self.H, self.I, dtype=self.grad_dtype, device=self.device)
+
+    def backward(self, dout: torch.Tensor, *, accumulate: bool = False):
+        """Gradients of the last forward: writes (or, accumulate, adds to) dw13 and
+        dw2 and returns (dx [T, H], dlogits [T, E]), or (dx, dtopk_weights [T, k])
+        where forward was given topk_ids.  The results are the layer's own buffers.
+
+        With a share of the experts, dx and dlogits are that share's part: both
+        add up over the shares.  What forward kept is used up: one backward for
+        each forward, and ids and weights given to forward must still be as
+        they were."""
+        if not self.train:
+            raise ValueError("the layer was made without train=True")
+        if self._saved is None:
+            raise ValueError("backward needs a forward of its own before it")
+        T, ids, tw, routed = self._saved
+        if dout.shape != (T, self.H):
+            raise ValueError(f"dout: want {(T, self.H)}, got {tuple(dout.shape)}")
+        if self.dw13 is None:
+            self.allocate_grads()
+        s2d, dx, dtw = self.src2dst[:T], self.dx[:T], self.dtopk_weights[:T]
+        m_idx, starts, counts = self.m_indices, self.expert_start_loc, self.num_valid
+        with self._mark("combine_bwd"):
+            L.moe_combine_bwd(dout, self.y, s2d, tw, self.dy, dtw)
+        self._saved = None
+        if routed:
+            with self._mark("route_bwd"):
+                L.moe_route_topk_bwd(ids, tw, dtw, self.dlogits[:T])
+        with self._mark("wgrad_w2"):
+            L.grouped_gemm_contig_wgrad(self.dy, self.act, starts, counts, self.dw2, accumulate)
+        dact = self.act          # the activation has been used: its buffer takes the gradient
+        with self._mark("dgrad_w2"):
+            L.grouped_gemm_contig_dgrad(self.dy, self.w2, dact, m_idx)
+        with self._mark("silu_bwd"):
+            L.silu_and_mul_bwd(self.gateup, dact, self.gateup, m_indices=m_idx)
+        with self._mark("wgrad_w13"):
+            L.grouped_gemm_contig_wgrad(self.gateup, self.x_buf, starts, counts, self.dw13, accumulate)
+        with self._mark("dgrad_w13"):
+            L.grouped_gemm_contig_dgrad(self.gateup, self.w13, self.y, m_idx)
+        with self._mark("scatter_bwd"):
+            L.moe_scatter_bwd(self.y, s2d, dx)
+        return dx, (self.dlogits[:T] if routed else dtw)
+
+    def optimizer(self, **kw) -> AdamW:
+        """AdamW (optim.AdamW's arguments) over the expert weights and their gradients."""
+        if not self.train:
+            raise ValueError("the layer was made without train=True")
+        if self.w13 is None:
+            raise ValueError("set the weights first: the masters are taken from them")
+        if self.dw13 is None:
+            self.allocate_grads()
+        return AdamW([self.w13, self.w2], [self.dw13, self.dw2], **kw)
 
 
 class _NoMark:

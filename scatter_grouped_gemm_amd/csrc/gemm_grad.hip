@@ -1,11 +1,33 @@
 // The two gradients of the compact grouped product C[r, :] = A[r, :] . B[g(r)]^T:
-//   dA[r, :] = dC[r, :] . B[g(r)]          (grouped_gemm_contig_dgrad)
-//   dB[g]    = sum over g's rows dC[r, :]^T A[r, :]   (grouped_gemm_contig_wgrad)
+//   dA[r, :] = dC[r, :] . B[g(r)]                     (grouped_gemm_contig_dgrad)
+//   dB[g]    = sum over g's rows of dC[r, :]^T A[r, :]   (grouped_gemm_contig_wgrad)
 // BF16 operands, fp32 accumulation.
 //
-// First form: 128 x 128 tiles, four wavefronts of 64 x 64, 32 steps of the
-// reduction at a time through LDS.
+// Both are tiles D[i, j] = sum_k P[i, k] Q[k, j] of 256 x 256 outputs.  Q is
+// stored with its reduction outermost in both (B [N][K] and A [rows][K]), P
+// along its reduction in dgrad (dC rows) and with it outermost in wgrad.
+//   - Operands with the reduction outermost go to LDS as they lie in memory and
+//     are transposed on the way out (ds_read_b64_tr_b16: 16 lanes read four rows
+//     of 16 values, each lane gets four values of one column).
+//   - Workgroup = 8 wavefronts in two groups of four, one wavefront of each
+//     group on every SIMD.  A wavefront owns 64 + 64 rows by 64 columns of the
+//     tile in four quadrants.  A step of 64 of the reduction is four phases, a
+//     phase is a load part (LDS reads, global loads) and an MFMA part (16
+//     instructions of one quadrant), each ended by a barrier; the second group
+//     runs half a phase behind the first, so on every SIMD one wavefront feeds
+//     the matrix core while the other one reads.
+//   - Global loads go straight to LDS.  Two stages; each piece of a stage (P's
+//     two halves, Q) is loaded again as soon as both groups have read it, which
+//     gives a load 1.25 to 1.75 steps (about 1 us) to arrive.
+//   - The phases of a step use the quadrants in the order P0 Q0, P0 Q1, P1 Q1,
+//     P1 Q0, and the next step starts with Q1: so the reads of a step spread
+//     over the phases as 8, 4, 8, 4 KB a wavefront and Q's registers need no copy.
+//   - The loop is one stream of steps over all of a workgroup's tiles: the loads
+//     cross into the next tile while the current one is finished.
+#include <mutex>
+
 #include "common.h"
+#include "gemm_runs.h"
 
 namespace moe {
 namespace {
@@ -13,13 +35,18 @@ namespace {
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 typedef __attribute__((ext_vector_type(4))) float f32x4;
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((ext_vector_type(8))) short s16x8;
 
-constexpr int kBK = 32, kPad = 8;
+constexpr int kThreads = 512;
+constexpr int kTileN = 256;
+constexpr int kStep = 64;   // of the reduction
+constexpr int kGroupN = 8;  // wgrad: tiles along N of a block of the tile order
 
 struct GradArgs {
-  const uint16_t* P;   // dC [M][N]
-  const uint16_t* Q;   // dgrad: B [G][N][K]; wgrad: A [M][K]
-  void* D;             // dgrad: dA [M][K]; wgrad: dB [G][N][K]
+  const uint8_t* P;   // dC [M][N]
+  const uint8_t* Q;   // dgrad: B [G][N][K]; wgrad: A [M][K]
+  void* D;            // dgrad: dA [M][K]; wgrad: dB [G][N][K]
   const int32_t* m_indices;
   const int32_t* starts;
   const int32_t* counts;
@@ -27,98 +54,377 @@ struct GradArgs {
   int N, K, G;
 };
 
-// LDS tiles hold [reduction][128 + pad]; a fragment is eight 2-byte reads.
-__device__ __forceinline__ bf16x8 frag(const uint16_t* t, int col, int k0) {
-  uint16_t v[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = t[(k0 + j) * (128 + kPad) + col];
-  return __builtin_bit_cast(bf16x8, v);
+using runs::wait_vm;
+
+__device__ __forceinline__ void fence() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+}
+// A barrier that nothing crosses.
+__device__ __forceinline__ void barrier() {
+  fence();
+  __builtin_amdgcn_s_barrier();
+  fence();
+}
+__device__ __forceinline__ void wait_lds() {
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+}
+
+// A tile as both sides of the stream see it.
+struct Tile {
+  int64_t row;  // dgrad: first row; wgrad: first row of the expert
+  int rows;     // dgrad: rows of the tile; wgrad: rows of the expert
+  int id, pt, qt, steps;
+};
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0,
+                                           static_cast<int>(bytes > 0 ? bytes : 0), 0x00020000);
+}
+
+__device__ __forceinline__ s16x4 read_tr(const uint8_t* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (__attribute__((address_space(3))) s16x4*)(p));
 }
 
 template <bool WGRAD, bool F32, bool ACC>
-__global__ __launch_bounds__(256) void gemm_grad_kernel(const GradArgs a) {
-  __shared__ uint16_t tp[kBK * (128 + kPad)], tq[kBK * (128 + kPad)];
-  __shared__ int valid;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+__global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  // P half h of stage s, Q of stage s.  Arrays of their own: the compiler then
+  // knows which loads to LDS a read can depend on.
+  __shared__ __attribute__((aligned(1024))) uint8_t p00[16384], p01[16384], p10[16384], p11[16384];
+  __shared__ __attribute__((aligned(1024))) uint8_t q0[32768], q1[32768];
+  __shared__ int4 table[WGRAD ? 1 : runs::kTable];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
   const int fr = lane & 15, fg = lane >> 4;
-  int64_t row0;  // first row of the tile (dgrad) or of the expert (wgrad)
-  int rows, e;
+  const int64_t ldp = static_cast<int64_t>(a.N) * 2, ldq = static_cast<int64_t>(a.K) * 2;  // bytes
+  const int ntk = (a.K + kTileN - 1) / kTileN;
+
+  // ======== the tiles of this workgroup ========
+  int pos, pos_end, stride, per = 0, ntn = 0;
+  int NR = 0, cur = 0;
+  const int xcd = blockIdx.x & 7;
   if constexpr (WGRAD) {
-    e = blockIdx.z;
-    int64_t s = a.starts[e], n = a.counts[e];
-    if (s < 0 || s > a.M) s = 0, n = 0;
-    if (n < 0) n = 0;
-    if (n > a.M - s) n = a.M - s;
-    row0 = s;
-    rows = static_cast<int>(n);
+    ntn = (a.N + kTileN - 1) / kTileN;
+    per = (ntn * ntk + 7) / 8;  // of each expert, for this XCD
+    pos = static_cast<int>(blockIdx.x >> 3);
+    pos_end = a.G * per;
+    stride = static_cast<int>(gridDim.x >> 3);
   } else {
-    row0 = static_cast<int64_t>(blockIdx.y) * 128;
-    if (tid == 0) valid = 0;
-    __syncthreads();
-    e = a.m_indices[row0];
-    if (e < 0 || e >= a.G) return;
-    if (tid < 128 && row0 + tid < a.M && a.m_indices[row0 + tid] >= 0) atomicAdd(&valid, 1);
-    __syncthreads();
-    rows = valid;
+    runs::Share sh;
+    static_assert(runs::kMaxBlocks * 4 <= 32768, "the set-up arrays fit in the stages");
+    if (!runs::build_share<8>(a.m_indices, a.M, a.G, ntk, reinterpret_cast<int*>(q0),
+                              reinterpret_cast<int*>(q1), reinterpret_cast<int*>(p00), table, sh))
+      return;
+    NR = sh.NR;
+    pos = sh.lo + static_cast<int>(blockIdx.x >> 3);
+    pos_end = sh.hi;
+    stride = sh.per_xcd;
   }
-  const int c0 = blockIdx.x * 128;                       // output columns
-  const int r0 = WGRAD ? static_cast<int>(blockIdx.y) * 128 : 0;  // output rows
-  const int red = WGRAD ? rows : a.N;                    // length of the reduction
-  const uint16_t* q = WGRAD ? a.Q + row0 * a.K : a.Q + static_cast<int64_t>(e) * a.N * a.K;
-  const uint16_t* p = a.P + row0 * a.N;
-  f32x4 acc[4][4] = {};
-  for (int k0 = 0; k0 < red; k0 += kBK) {
-    __syncthreads();
-    for (int i = tid; i < kBK * 128; i += 256) {
-      const int k = i >> 7, c = i & 127;
-      const bool in = k0 + k < red;
-      tq[k * (128 + kPad) + c] = in ? q[static_cast<int64_t>(k0 + k) * a.K + c0 + c] : 0;
-      if constexpr (WGRAD)
-        tp[k * (128 + kPad) + c] = in ? p[static_cast<int64_t>(k0 + k) * a.N + r0 + c] : 0;
-    }
-    if constexpr (!WGRAD)
-      for (int i = tid; i < kBK * 128; i += 256) {
-        const int r = i >> 5, k = i & 31;
-        tp[k * (128 + kPad) + r] = r < rows ? p[static_cast<int64_t>(r) * a.N + k0 + k] : 0;
+  // The tile at pos or the next one with work; false: none left.
+  auto fetch = [&](int& at, int& c, Tile& t) __attribute__((always_inline)) -> bool {
+    for (; at < pos_end; at += stride) {
+      if constexpr (WGRAD) {
+        const int e = at / per, i = xcd * per + (at - e * per);
+        if (i >= ntn * ntk) continue;
+        int64_t s = a.starts[e], n = a.counts[e];
+        if (s < 0 || s > a.M || n < 0) s = 0, n = 0;
+        n = n < a.M - s ? n : a.M - s;
+        if (ACC && n == 0) continue;
+        const int grp = i / (kGroupN * ntk), p0 = grp * kGroupN;
+        const int gs = ntn - p0 < kGroupN ? ntn - p0 : kGroupN;
+        const int r = i - p0 * ntk;
+        t.row = s;
+        t.rows = static_cast<int>(n);
+        t.id = e;
+        t.qt = r / gs;
+        t.pt = p0 + r - t.qt * gs;
+        t.steps = n > 0 ? static_cast<int>((n + kStep - 1) / kStep) : 1;
+        return true;
+      } else {
+        const runs::Tile r = runs::decode<16>(table, NR, c, at, ntk);
+        if (r.rows <= 0) continue;
+        t.row = r.row;
+        t.rows = r.rows;
+        t.id = r.id;
+        t.pt = 0;
+        t.qt = r.nt;
+        t.steps = a.N / kStep;
+        return true;
       }
-    __syncthreads();
-    bf16x8 fp[4], fq[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      fp[i] = frag(tp, (wave >> 1) * 64 + i * 16 + fr, fg * 8);
-      fq[i] = frag(tq, (wave & 1) * 64 + i * 16 + fr, fg * 8);
     }
-    // D^T: the lane ends with four consecutive columns of one output row
+    return false;
+  };
+  Tile lt;  // load side
+  if (!fetch(pos, cur, lt)) return;
+  Tile ct = lt;  // compute side
+  int cpos = pos, ccur = cur;
+
+  // ======== load side ========
+  // offsets of this lane's 16 bytes within a step of the operand; a load fills
+  // 1 KB of LDS in lane order, so the order of the 32-byte pieces (16-byte
+  // pieces in dgrad's P) is permuted here, at the source
+  uint32_t vp[2], vq[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[j], fp[i], acc[i][j], 0, 0, 0);
+  for (int j = 0; j < 2; ++j) {
+    if constexpr (WGRAD) {
+      const int r = wave * 8 + j * 4 + (lane >> 4);
+      const int f = (r & 3) | (((r >> 3) & 1) << 2);
+      vp[j] = static_cast<uint32_t>(r * ldp) + ((((lane & 15) >> 1) ^ f) << 5) + ((lane & 1) << 4);
+    } else {
+      const int r = (wave * 2 + j) * 8 + (lane >> 3);
+      vp[j] = static_cast<uint32_t>(r * ldp) + (((lane & 7) ^ (lane >> 3)) << 4);
+    }
   }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = wave * 8 + j * 2 + (lane >> 5);
+    const int f = (r & 3) | (((r >> 3) & 1) << 2);
+    vq[j] = static_cast<uint32_t>(r * ldq) + ((((lane & 31) >> 1) ^ f) << 5) + ((lane & 1) << 4);
+  }
+  const uint8_t *bp = nullptr, *bq = nullptr;  // this step's operands
+  int64_t np0 = 0, np1 = 0, nq = 0;            // and the bytes within bounds
+  int lk = 0;
+  auto lset = [&]() __attribute__((always_inline)) {
+    if constexpr (WGRAD) {
+      const int64_t r0 = static_cast<int64_t>(lk) * kStep;
+      int64_t v = lt.rows - r0;
+      v = v < kStep ? v : kStep;
+      bp = a.P + (lt.row + r0) * ldp + lt.pt * (kTileN * 2);
+      np0 = v * ldp - lt.pt * (kTileN * 2);
+      bq = a.Q + (lt.row + r0) * ldq + lt.qt * (kTileN * 2);
+      nq = v * ldq - lt.qt * (kTileN * 2);
+    } else {
+      bp = a.P + lt.row * ldp + lk * (kStep * 2);
+      np0 = (lt.rows < 128 ? lt.rows : 128) * ldp - lk * (kStep * 2);
+      np1 = (lt.rows - 128) * ldp - lk * (kStep * 2);
+      bq = a.Q + (static_cast<int64_t>(lt.id) * a.N + lk * kStep) * ldq + lt.qt * (kTileN * 2);
+      nq = kStep * ldq - lt.qt * (kTileN * 2);
+    }
+  };
+  lset();
+  // No immediate offset in these loads: the instruction adds it to the LDS
+  // address too.
+  auto to_lds = [&](__amdgpu_buffer_rsrc_t rs, uint8_t* dst, uint32_t off) __attribute__((always_inline)) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16, off, 0, 0, 0);
+  };
+  auto load_p = [&](uint8_t* dst, int half) __attribute__((always_inline)) {
+    const int64_t skip = half ? (WGRAD ? 256 : 128 * ldp) : 0;
+    const auto rs = buffer(bp + skip, WGRAD ? np0 - skip : (half ? np1 : np0));
+#pragma unroll
+    for (int j = 0; j < 2; ++j) to_lds(rs, dst + (wave * 2 + j) * 1024, vp[j]);
+  };
+  auto load_q = [&](uint8_t* dst) __attribute__((always_inline)) {
+    const auto rs = buffer(bq, nq);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) to_lds(rs, dst + (wave * 4 + j) * 1024, vq[j]);
+  };
+  // on to the next step; behind the last tile its last step is read again (and
+  // never used), so that every step issues the same loads
+  auto advance = [&]() __attribute__((always_inline)) {
+    if (++lk == lt.steps) {
+      int np = pos + stride;
+      Tile t = lt;
+      if (fetch(np, cur, t)) {
+        pos = np;
+        lt = t;
+        lk = 0;
+      } else {
+        lk = lt.steps - 1;
+      }
+    }
+    lset();
+  };
+
+  // ======== compute side ========
+  // LDS offsets of this lane's part of a fragment.  tr: rows 8 fg + fr / 4 (and
+  // + 4) of the 32 of an MFMA, four values of column group fr & 3.
+  const int tr_row = fg * 8 + (fr >> 2);
+  const int tr_f = (tr_row & 3) | (((tr_row >> 3) & 1) << 2);
+  uint32_t op[4], oq[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = (wave >> 1) * 64 + i * 16 + fr;
-    if (!WGRAD && r >= rows) continue;
-    const int64_t orow = WGRAD ? static_cast<int64_t>(e) * a.N + r0 + r : row0 + r;
+    // dgrad: one piece of 16 bytes for each half of the step, blocks 2 KB apart
+    if constexpr (WGRAD)
+      op[i] = tr_row * 256 + (((wm * 4 + i) ^ tr_f) << 5) + (fr & 3) * 8;
+    else
+      op[i] = (wm * 64 + fr) * 128 + ((((i & 1) * 4 + fg) ^ (fr & 7)) << 4);
+    oq[i] = tr_row * 512 + (((wn * 4 + i) ^ tr_f) << 5) + (fr & 3) * 8;
+  }
+  // Keeps the compiler from working out the address in every array before the
+  // loop (and spilling them): from here on it has to add the array's place in
+  // the instruction's offset.
+  auto hold = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t o = orow * a.K + c0 + (wave & 1) * 64 + j * 16 + fg * 4;
-      f32x4 v = acc[i][j];
-      if constexpr (F32) {
-        f32x4* d = reinterpret_cast<f32x4*>(static_cast<float*>(a.D) + o);
-        if constexpr (ACC) v += *d;
-        *d = v;
-      } else {
-        uint2* d = reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.D) + o);
-        if constexpr (ACC) {
-          const uint2 b = *d;
-          v += f32x4{__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xffff0000u),
-                     __uint_as_float(b.y << 16), __uint_as_float(b.y & 0xffff0000u)};
+    for (int i = 0; i < (WGRAD ? 4 : 2); ++i) asm volatile("" : "+v"(op[i]));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(oq[i]));
+  };
+
+  bf16x8 fp[2][4];     // P half in use: [k half][16-row block]
+  bf16x8 fq[2][2][2];  // Q half: [half][k half][16-column block]
+  f32x4 acc[2][2][4][2] = {};
+  auto pair = [](s16x4 lo, s16x4 hi) __attribute__((always_inline)) {
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  auto read_p = [&](const uint8_t* s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (WGRAD)
+          fp[k][i] = pair(read_tr(s + op[i] + k * 8192), read_tr(s + op[i] + k * 8192 + 1024));
+        else
+          fp[k][i] = *reinterpret_cast<const bf16x8*>(s + op[k] + i * 2048);
+      }
+  };
+  auto read_q = [&](const uint8_t* s, int h) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        fq[h][k][j] = pair(read_tr(s + oq[h * 2 + j] + k * 16384), read_tr(s + oq[h * 2 + j] + k * 16384 + 2048));
+  };
+  // D^T: a lane ends with four consecutive columns of one row
+  auto mma = [&](int hp, int hq) __attribute__((always_inline)) {
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[hp][hq][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[hq][k][j], fp[k][i], acc[hp][hq][i][j], 0, 0, 0);
+    __builtin_amdgcn_s_setprio(0);
+  };
+
+  auto epilogue = [&]() __attribute__((always_inline)) {
+    constexpr int ES = F32 ? 4 : 2;
+    const int col0 = ct.qt * kTileN + wn * 64;
+    // the lane's place, worked out here: kept over the loop it would cost the
+    // registers that the fragments need
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    const int row = l & 15;
+    const uint32_t lane_off = static_cast<uint32_t>((row * static_cast<int64_t>(a.K) + (l >> 4) * 4) * ES);
+    if (col0 < a.K) {
+#pragma unroll
+      for (int hp = 0; hp < 2; ++hp) {
+        const int r0 = hp * 128 + wm * 64;  // of the tile
+        const int64_t first = WGRAD ? static_cast<int64_t>(ct.id) * a.N + ct.pt * kTileN + r0 : ct.row + r0;
+        const int left = WGRAD ? a.N - ct.pt * kTileN - r0 : ct.rows - r0;
+        uint8_t* const base = static_cast<uint8_t*>(a.D) + (first * a.K + col0) * ES;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (i * 16 + row < left) {
+            uint8_t* const line = base + i * 16 * static_cast<int64_t>(a.K) * ES;
+#pragma unroll
+            for (int hq = 0; hq < 2; ++hq)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                f32x4 v = acc[hp][hq][i][j];
+                uint8_t* const at = line + lane_off + (hq * 32 + j * 16) * ES;
+                if constexpr (F32) {
+                  f32x4* d = reinterpret_cast<f32x4*>(at);
+                  if constexpr (ACC) v += *d;
+                  *d = v;
+                } else {
+                  uint2* d = reinterpret_cast<uint2*>(at);
+                  if constexpr (ACC) {
+                    const uint2 b = *d;
+                    v += f32x4{__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xffff0000u),
+                               __uint_as_float(b.y << 16), __uint_as_float(b.y & 0xffff0000u)};
+                  }
+                  *d = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+                }
+              }
+          }
         }
-        *d = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
       }
     }
+#pragma unroll
+    for (int hp = 0; hp < 2; ++hp)
+#pragma unroll
+      for (int hq = 0; hq < 2; ++hq)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[hp][hq][i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+
+  // ======== the stream ========
+  int ck = 0;
+  bool more = true;
+  // One step from stage S, starting with Q's half S.  Each wait is for loads
+  // whose data is read one phase later: the barrier behind it makes them
+  // visible to both groups before the first one reads.
+  auto step = [&](uint8_t* ps0, uint8_t* ps1, uint8_t* qs, uint8_t* qn, int S) __attribute__((always_inline)) {
+    // phase 0
+    hold();
+    read_p(ps0);
+    wait_lds();
+    barrier();
+    mma(0, S);
+    barrier();
+    // phase 1: P half 0 of this stage is free
+    read_q(qs, 1 - S);
+    load_p(ps0, 0);
+    wait_lds();
+    wait_vm<10>();  // P half 1 of this step
+    barrier();
+    mma(0, 1 - S);
+    barrier();
+    // phase 2: so is Q
+    read_p(ps1);
+    load_q(qs);
+    wait_lds();
+    wait_vm<8>();  // Q and P half 0 of the next step
+    barrier();
+    mma(1, 1 - S);
+    barrier();
+    // phase 3
+    read_q(qn, 1 - S);
+    load_p(ps1, 1);
+    advance();
+    wait_lds();
+    barrier();
+    mma(1, S);
+    if (++ck == ct.steps) {
+      fence();
+      epilogue();
+      ck = 0;
+      cpos += stride;
+      more = fetch(cpos, ccur, ct);
+    }
+    barrier();
+  };
+
+  load_p(p00, 0);
+  load_q(q0);
+  load_p(p10, 1);
+  advance();
+  load_p(p01, 0);
+  load_q(q1);
+  load_p(p11, 1);
+  advance();
+  wait_vm<8>();
+  barrier();
+  read_q(q0, 0);
+  wait_lds();
+  barrier();
+  if (wm == 1) __builtin_amdgcn_s_barrier();  // half a phase behind
+  for (;;) {
+    step(p00, p10, q0, q1, 0);
+    if (!more) break;
+    step(p01, p11, q1, q0, 1);
+    if (!more) break;
   }
+  if (wm == 0) __builtin_amdgcn_s_barrier();
+  wait_vm<0>();  // the loads behind the last step
+#endif
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -126,9 +432,35 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 int32_t check_sizes(int64_t M, int32_t N, int32_t K, int32_t G) {
   if (M < 0 || N <= 0 || K <= 0 || G < 0) return MOE_EINVAL;
   if (N % 128 != 0 || K % 128 != 0) return MOE_EUNSUPPORTED;
-  // a 64-row panel of an operand is addressed with 32-bit offsets
+  // 256 rows of an operand are addressed with 32-bit offsets
   if (N > (1 << 22) || K > (1 << 22)) return MOE_EUNSUPPORTED;
-  if ((M + 127) / 128 > 8176 || G > 1024) return MOE_EUNSUPPORTED;
+  if ((M + 127) / 128 > runs::kMaxBlocks || G > 1024) return MOE_EUNSUPPORTED;
+  // tile positions
+  if (((static_cast<int64_t>(N) + 255) / 256) * ((K + 255) / 256) / 8 * G >= (1 << 30)) return MOE_EUNSUPPORTED;
+  if ((static_cast<int64_t>(K) + 255) / 256 * ((M + 127) / 128) >= (1 << 30)) return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
+// One workgroup per CU, a multiple of 8 (one share of the tiles per XCD).
+int grid_size() {
+  static int grid[64] = {0};
+  static std::once_flag once[64];
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 0;
+  std::call_once(once[dev], [dev]() {
+    int cus = 0;
+    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess)
+      grid[dev] = cus >= 8 ? cus / 8 * 8 : 8;
+  });
+  return grid[dev];
+}
+
+template <bool WGRAD, bool F32, bool ACC>
+int32_t launch(const GradArgs& a, void* stream) {
+  const int grid = grid_size();
+  if (grid == 0) return MOE_EDEVICE;
+  gemm_grad_kernel<WGRAD, F32, ACC><<<grid, kThreads, 0, static_cast<hipStream_t>(stream)>>>(a);
+  MOE_CHECK_LAUNCH();
   return MOE_OK;
 }
 
@@ -145,12 +477,9 @@ extern "C" int32_t grouped_gemm_contig_dgrad(const void* dC, const void* B, void
   if (M == 0 || G == 0) return MOE_OK;
   if (!dC || !B || !dA || !m_indices) return MOE_EINVAL;
   if (!aligned16(dC) || !aligned16(B) || !aligned16(dA)) return MOE_EUNSUPPORTED;
-  const GradArgs a{static_cast<const uint16_t*>(dC), static_cast<const uint16_t*>(B), dA, m_indices, nullptr,
+  const GradArgs a{static_cast<const uint8_t*>(dC), static_cast<const uint8_t*>(B), dA, m_indices, nullptr,
                    nullptr, M, N, K, G};
-  const dim3 grid(K / 128, static_cast<unsigned>((M + 127) / 128), 1);
-  gemm_grad_kernel<false, false, false><<<grid, 256, 0, static_cast<hipStream_t>(stream)>>>(a);
-  MOE_CHECK_LAUNCH();
-  return MOE_OK;
+  return launch<false, false, false>(a, stream);
 }
 
 extern "C" int32_t grouped_gemm_contig_wgrad(const void* dC, const void* A,
@@ -164,17 +493,9 @@ extern "C" int32_t grouped_gemm_contig_wgrad(const void* dC, const void* A,
   if (G == 0) return MOE_OK;
   if (!expert_start_loc || !num_valid || !dB || (M > 0 && (!dC || !A))) return MOE_EINVAL;
   if (!aligned16(dC) || !aligned16(A) || !aligned16(dB)) return MOE_EUNSUPPORTED;
-  const GradArgs a{static_cast<const uint16_t*>(dC), static_cast<const uint16_t*>(A), dB, nullptr,
+  const GradArgs a{static_cast<const uint8_t*>(dC), static_cast<const uint8_t*>(A), dB, nullptr,
                    expert_start_loc, num_valid, M, N, K, G};
-  const dim3 grid(K / 128, N / 128, G);
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  if (out_dtype == MOE_DTYPE_FP32) {
-    if (accumulate) gemm_grad_kernel<true, true, true><<<grid, 256, 0, s>>>(a);
-    else gemm_grad_kernel<true, true, false><<<grid, 256, 0, s>>>(a);
-  } else {
-    if (accumulate) gemm_grad_kernel<true, false, true><<<grid, 256, 0, s>>>(a);
-    else gemm_grad_kernel<true, false, false><<<grid, 256, 0, s>>>(a);
-  }
-  MOE_CHECK_LAUNCH();
-  return MOE_OK;
+  if (out_dtype == MOE_DTYPE_FP32)
+    return accumulate ? launch<true, true, true>(a, stream) : launch<true, true, false>(a, stream);
+  return accumulate ? launch<true, false, true>(a, stream) : launch<true, false, false>(a, stream);
 }

@@ -1,5 +1,5 @@
 // Tile order of the compact-layout register-streamed grouped GEMM
-// (gemm_wreg.hip): the run table each workgroup builds from m_indices, the
+// (gemm_wreg.hip) and of its input gradient (gemm_grad.hip): the run table each workgroup builds from m_indices, the
 // position -> tile decoder, and the small LDS and wait helpers the kernel uses
 // around it.
 //
@@ -47,7 +47,8 @@ __device__ __forceinline__ int4 lds_read_run(const int4* t) {
   return v;
 }
 
-// exclusive scans over the workgroup's 256 threads (scr: 8 ints of LDS)
+// exclusive scans over the workgroup's WAVES wavefronts (scr: 2 * WAVES ints of LDS)
+template <int WAVES>
 __device__ __forceinline__ int scan_excl_max(int v, int* scr) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   int inc = v;
@@ -64,6 +65,7 @@ __device__ __forceinline__ int scan_excl_max(int v, int* scr) {
   __syncthreads();
   return ex;
 }
+template <int WAVES>
 __device__ __forceinline__ int2 scan_excl_sum2(int a, int b, int* scr, int2& total) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   int ia = a, ib = b;
@@ -81,7 +83,7 @@ __device__ __forceinline__ int2 scan_excl_sum2(int a, int b, int* scr, int2& tot
   }
   __syncthreads();
   int pa = 0, pb = 0, ta = 0, tb = 0;
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < WAVES; ++q) {
     if (q < w) {
       pa += scr[2 * q];
       pb += scr[2 * q + 1];
@@ -146,17 +148,17 @@ struct Share {
 };
 
 // Builds the run table of this workgroup's XCD share into `table` (kTable
-// entries of LDS), using `scratch` (kSetupBytes of LDS, free afterwards) for
-// the per-block ids.  All 256 threads call it; it ends with a barrier.
-// Returns false when the workgroup has no position to run.
+// entries of LDS), using three pieces of LDS (free afterwards): the first-row
+// ids and the valid rows of the run ending at each 128-row block (kMaxBlocks
+// ints each) and 2 * WAVES ints for the scans.  All 64 * WAVES threads call it;
+// it ends with a barrier.  Returns false when the workgroup has no position to
+// run.
+template <int WAVES>
 __device__ __forceinline__ bool build_share(const int32_t* __restrict__ m_indices, int64_t M, int G,
-                                            int ntn, uint8_t* scratch, int4* table, Share& sh) {
-  constexpr int kThreads = 256;
+                                            int ntn, int* ids, int* zv, int* scr, int4* table, Share& sh) {
+  constexpr int kThreads = 64 * WAVES;
   const int tid = threadIdx.x;
   const int nblk = static_cast<int>((M + 127) / 128);
-  int* const ids = reinterpret_cast<int*>(scratch);  // [nblk] first-row ids
-  int* const scr = ids + kMaxBlocks + 8;
-  int* const zv = scr + 16;  // [nblk] valid rows of the run ending at block j
   for (int j = tid; j < nblk; j += kThreads) {
     const int v = m_indices[static_cast<int64_t>(j) * 128];
     ids[j] = (v >= 0 && v < G) ? v : -1;
@@ -169,7 +171,7 @@ __device__ __forceinline__ bool build_share(const int32_t* __restrict__ m_indice
   int ls = -1;
   for (int j = j0; j < j1; ++j)
     if (ids[j] >= 0 && (j == 0 || ids[j - 1] != ids[j])) ls = j;
-  const int carry = max(scan_excl_max(ls, scr), -1);
+  const int carry = max(scan_excl_max<WAVES>(ls, scr), -1);
   // runs ending in this thread's blocks: their valid rows (the last block's
   // valid rows come first, so a binary search for its first negative entry)
   // and M-tiles
@@ -195,7 +197,7 @@ __device__ __forceinline__ bool build_share(const int32_t* __restrict__ m_indice
     }
   }
   int2 tot;
-  const int2 base = scan_excl_sum2(cnt, tsum, scr, tot);
+  const int2 base = scan_excl_sum2<WAVES>(cnt, tsum, scr, tot);
   const int U = tot.y * ntn;  // positions of the whole order
   const int per_xcd = gridDim.x >> 3;
   const int xcd = blockIdx.x & 7;
@@ -217,7 +219,7 @@ __device__ __forceinline__ bool build_share(const int32_t* __restrict__ m_indice
     }
   }
   int2 cc;
-  scan_excl_sum2(c_lo, c_hi, scr, cc);
+  scan_excl_sum2<WAVES>(c_lo, c_hi, scr, cc);
   const int R0 = cc.x, NR = cc.y - cc.x;
   {
     int S = carry, mb = base.y, ri = base.x;
@@ -241,6 +243,14 @@ __device__ __forceinline__ bool build_share(const int32_t* __restrict__ m_indice
   sh.hi = hi_x;
   sh.per_xcd = per_xcd;
   return NR > 0 && NR <= kTable && lo_x + static_cast<int>(blockIdx.x >> 3) < hi_x;
+}
+
+// The same for 256 threads with one contiguous piece of scratch (kSetupBytes).
+__device__ __forceinline__ bool build_share(const int32_t* __restrict__ m_indices, int64_t M, int G,
+                                            int ntn, uint8_t* scratch, int4* table, Share& sh) {
+  int* const ids = reinterpret_cast<int*>(scratch);
+  int* const scr = ids + kMaxBlocks + 8;
+  return build_share<4>(m_indices, M, G, ntn, ids, scr + 16, scr, table, sh);
 }
 
 }  // namespace runs

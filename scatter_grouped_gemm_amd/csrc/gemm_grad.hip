@@ -77,9 +77,31 @@ struct Tile {
   int id, pt, qt, steps;
 };
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t* base, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0,
-                                           static_cast<int>(bytes > 0 ? bytes : 0), 0x00020000);
+// No more than `bytes` from base: reads behind them give zeros, writes are dropped.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t* base, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, bytes > 0 ? bytes : 0, 0x00020000);
+}
+
+// A copy that the compiler takes for a new value.  What is worked out from it
+// once in a tile would otherwise be kept in registers over the whole loop, and
+// there are more such values than registers.
+__device__ __forceinline__ int fresh_copy(int x) {
+  asm volatile("" : "+s"(x));
+  return x;
+}
+
+// Exchanges a of the lanes 16 .. 31 (48 .. 63) with b of the lanes 0 .. 15
+// (32 .. 47), and c with d: (a, b, c, d) afterwards.
+__device__ __forceinline__ f32x4 swap_rows(float a, float b, float c, float d) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  const auto q = __builtin_amdgcn_permlane16_swap(__float_as_uint(c), __float_as_uint(d), false, false);
+  return f32x4{__uint_as_float(r[0]), __uint_as_float(r[1]), __uint_as_float(q[0]), __uint_as_float(q[1])};
+}
+
+// An int that no kernel writes, through the scalar cache: a vector load would
+// make the wavefront wait for all its loads to LDS.
+__device__ __forceinline__ int scalar_load(const int32_t* p) {
+  return *(const __attribute__((address_space(4))) int32_t*)(reinterpret_cast<uintptr_t>(p));
 }
 
 __device__ __forceinline__ s16x4 read_tr(const uint8_t* p) {
@@ -128,15 +150,16 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
   auto fetch = [&](int& at, int& c, Tile& t) __attribute__((always_inline)) -> bool {
     for (; at < pos_end; at += stride) {
       if constexpr (WGRAD) {
-        const int e = at / per, i = xcd * per + (at - e * per);
-        if (i >= ntn * ntk) continue;
-        int64_t s = a.starts[e], n = a.counts[e];
+        const int per_ = fresh_copy(per), ntk_ = fresh_copy(ntk), ntn_ = fresh_copy(ntn);
+        const int e = at / per_, i = xcd * per_ + (at - e * per_);
+        if (i >= ntn_ * ntk_) continue;
+        int64_t s = scalar_load(a.starts + e), n = scalar_load(a.counts + e);
         if (s < 0 || s > a.M || n < 0) s = 0, n = 0;
         n = n < a.M - s ? n : a.M - s;
         if (ACC && n == 0) continue;
-        const int grp = i / (kGroupN * ntk), p0 = grp * kGroupN;
-        const int gs = ntn - p0 < kGroupN ? ntn - p0 : kGroupN;
-        const int r = i - p0 * ntk;
+        const int grp = i / (kGroupN * ntk_), p0 = grp * kGroupN;
+        const int gs = ntn_ - p0 < kGroupN ? ntn_ - p0 : kGroupN;
+        const int r = i - p0 * ntk_;
         t.row = s;
         t.rows = static_cast<int>(n);
         t.id = e;
@@ -145,7 +168,7 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
         t.steps = n > 0 ? static_cast<int>((n + kStep - 1) / kStep) : 1;
         return true;
       } else {
-        const runs::Tile r = runs::decode<16>(table, NR, c, at, ntk);
+        const runs::Tile r = runs::decode<16>(table, NR, c, at, fresh_copy(ntk));
         if (r.rows <= 0) continue;
         t.row = r.row;
         t.rows = r.rows;
@@ -185,24 +208,30 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
     const int f = (r & 3) | (((r >> 3) & 1) << 2);
     vq[j] = static_cast<uint32_t>(r * ldq) + ((((lane & 31) >> 1) ^ f) << 5) + ((lane & 1) << 4);
   }
-  const uint8_t *bp = nullptr, *bq = nullptr;  // this step's operands
-  int64_t np0 = 0, np1 = 0, nq = 0;            // and the bytes within bounds
+  const uint8_t *bp, *bq;  // this step's operands
+  int np, nq;              // and the bytes within bounds (dgrad: of P's first half)
+  int np1 = 0;             // dgrad: of P's second half
+  int left;                // wgrad: rows from here on
   int lk = 0;
+  // 64 rows of an operand are below 2^30 bytes, 128 below 2^31
+  auto lbound = [&]() __attribute__((always_inline)) {
+    const int v = left < kStep ? left : kStep;
+    np = v * static_cast<int>(ldp) - lt.pt * (kTileN * 2);
+    nq = v * static_cast<int>(ldq) - lt.qt * (kTileN * 2);
+  };
   auto lset = [&]() __attribute__((always_inline)) {
+    const int64_t lp = fresh_copy(a.N) * 2ll, lq = fresh_copy(a.K) * 2ll;
     if constexpr (WGRAD) {
-      const int64_t r0 = static_cast<int64_t>(lk) * kStep;
-      int64_t v = lt.rows - r0;
-      v = v < kStep ? v : kStep;
-      bp = a.P + (lt.row + r0) * ldp + lt.pt * (kTileN * 2);
-      np0 = v * ldp - lt.pt * (kTileN * 2);
-      bq = a.Q + (lt.row + r0) * ldq + lt.qt * (kTileN * 2);
-      nq = v * ldq - lt.qt * (kTileN * 2);
+      bp = a.P + lt.row * lp + lt.pt * (kTileN * 2);
+      bq = a.Q + lt.row * lq + lt.qt * (kTileN * 2);
+      left = lt.rows;
+      lbound();
     } else {
-      bp = a.P + lt.row * ldp + lk * (kStep * 2);
-      np0 = (lt.rows < 128 ? lt.rows : 128) * ldp - lk * (kStep * 2);
-      np1 = (lt.rows - 128) * ldp - lk * (kStep * 2);
-      bq = a.Q + (static_cast<int64_t>(lt.id) * a.N + lk * kStep) * ldq + lt.qt * (kTileN * 2);
-      nq = kStep * ldq - lt.qt * (kTileN * 2);
+      bp = a.P + lt.row * lp;
+      bq = a.Q + static_cast<int64_t>(lt.id) * a.N * lq + lt.qt * (kTileN * 2);
+      np = (lt.rows < 128 ? lt.rows : 128) * static_cast<int>(lp);
+      np1 = (lt.rows - 128) * static_cast<int>(lp);
+      nq = kStep * static_cast<int>(lq) - lt.qt * (kTileN * 2);
     }
   };
   lset();
@@ -212,8 +241,7 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16, off, 0, 0, 0);
   };
   auto load_p = [&](uint8_t* dst, int half) __attribute__((always_inline)) {
-    const int64_t skip = half ? (WGRAD ? 256 : 128 * ldp) : 0;
-    const auto rs = buffer(bp + skip, WGRAD ? np0 - skip : (half ? np1 : np0));
+    const auto rs = !half ? buffer(bp, np) : WGRAD ? buffer(bp + 256, np - 256) : buffer(bp + 128 * ldp, np1);
 #pragma unroll
     for (int j = 0; j < 2; ++j) to_lds(rs, dst + (wave * 2 + j) * 1024, vp[j]);
   };
@@ -226,17 +254,26 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
   // never used), so that every step issues the same loads
   auto advance = [&]() __attribute__((always_inline)) {
     if (++lk == lt.steps) {
-      int np = pos + stride;
+      int next = pos + stride;
       Tile t = lt;
-      if (fetch(np, cur, t)) {
-        pos = np;
+      if (fetch(next, cur, t)) {
+        pos = next;
         lt = t;
         lk = 0;
+        lset();
       } else {
         lk = lt.steps - 1;
       }
+    } else {
+      bq += kStep * ldq;
+      if constexpr (WGRAD) {
+        bp += kStep * ldp;
+        left -= kStep;
+        lbound();
+      } else {
+        bp += kStep * 2;
+      }
     }
-    lset();
   };
 
   // ======== compute side ========
@@ -301,50 +338,83 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
     __builtin_amdgcn_s_setprio(0);
   };
 
+  // Stores of the finished tile, then zero accumulators.  Every wavefront
+  // issues the same number of them whatever its tile holds (rows and columns
+  // outside fall outside the buffer and are dropped), so that the waits of the
+  // next steps can count them.
   auto epilogue = [&]() __attribute__((always_inline)) {
     constexpr int ES = F32 ? 4 : 2;
+    const int K = fresh_copy(a.K), N = fresh_copy(a.N);
     const int col0 = ct.qt * kTileN + wn * 64;
     // the lane's place, worked out here: kept over the loop it would cost the
     // registers that the fragments need
     int l = lane;
     asm volatile("" : "+v"(l));
-    const int row = l & 15;
-    const uint32_t lane_off = static_cast<uint32_t>((row * static_cast<int64_t>(a.K) + (l >> 4) * 4) * ES);
-    if (col0 < a.K) {
+    const int row = l & 15, g = l >> 4;
+    // fp32: four consecutive columns of each 16-column block.  bf16: eight, of
+    // block 0 in even lane groups and of block 1 in odd ones (see below).
+    const int col = F32 ? g * 4 : (g & 1) * 16 + (g >> 1) * 8;
+    const int line = K * ES;  // 64 rows of it are at most 2^30 bytes
+    const uint32_t off = row * line + col * ES;
 #pragma unroll
-      for (int hp = 0; hp < 2; ++hp) {
-        const int r0 = hp * 128 + wm * 64;  // of the tile
-        const int64_t first = WGRAD ? static_cast<int64_t>(ct.id) * a.N + ct.pt * kTileN + r0 : ct.row + r0;
-        const int left = WGRAD ? a.N - ct.pt * kTileN - r0 : ct.rows - r0;
-        uint8_t* const base = static_cast<uint8_t*>(a.D) + (first * a.K + col0) * ES;
+    for (int hp = 0; hp < 2; ++hp) {
+      const int r0 = hp * 128 + wm * 64;  // of the tile
+      const int64_t first = WGRAD ? static_cast<int64_t>(ct.id) * N + ct.pt * kTileN + r0 : ct.row + r0;
+      int rows = WGRAD ? N - ct.pt * kTileN - r0 : ct.rows - r0;
+      rows = rows < 64 ? rows : 64;
+      const int bytes = col0 < K && rows > 0 ? rows * line - col0 * ES : 0;
+      const auto rd = buffer(static_cast<uint8_t*>(a.D) + first * line + col0 * ES, bytes);
+      constexpr int NJ = F32 ? 2 : 1;  // 16-byte accesses of 32 columns
+      u32x4 old[4][2][NJ];
+      if constexpr (ACC) {  // all of a half in flight together
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (i * 16 + row < left) {
-            uint8_t* const line = base + i * 16 * static_cast<int64_t>(a.K) * ES;
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int hq = 0; hq < 2; ++hq)
+          for (int hq = 0; hq < 2; ++hq)
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                f32x4 v = acc[hp][hq][i][j];
-                uint8_t* const at = line + lane_off + (hq * 32 + j * 16) * ES;
-                if constexpr (F32) {
-                  f32x4* d = reinterpret_cast<f32x4*>(at);
-                  if constexpr (ACC) v += *d;
-                  *d = v;
-                } else {
-                  uint2* d = reinterpret_cast<uint2*>(at);
-                  if constexpr (ACC) {
-                    const uint2 b = *d;
-                    v += f32x4{__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xffff0000u),
-                               __uint_as_float(b.y << 16), __uint_as_float(b.y & 0xffff0000u)};
-                  }
-                  *d = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-                }
-              }
+            for (int j = 0; j < NJ; ++j)
+              old[i][hq][j] = __builtin_amdgcn_raw_buffer_load_b128(rd, off + i * 16 * line + hq * 32 * ES + j * 64, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int hq = 0; hq < 2; ++hq) {
+          const uint32_t at = off + i * 16 * line + hq * 32 * ES;
+          f32x4 v0 = acc[hp][hq][i][0], v1 = acc[hp][hq][i][1];
+          if constexpr (F32) {
+            if constexpr (ACC) {
+              v0 += __builtin_bit_cast(f32x4, old[i][hq][0]);
+              v1 += __builtin_bit_cast(f32x4, old[i][hq][NJ - 1]);
+            }
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v0), rd, at, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v1), rd, at + 64, 0, 0);
+          } else {
+            // Lanes of an odd group swap their part of block 0 for the part of
+            // block 1 that the group before them holds: eight columns in a row
+            // for one 16-byte access.  Where the old value has to be added,
+            // this is done in fp32, so that the sum is rounded once.
+            u32x4 o;
+            if constexpr (ACC) {
+              const auto add = [&](uint32_t w, float lo, float hi) __attribute__((always_inline)) {
+                return pack_bf16x2(lo + __uint_as_float(w << 16), hi + __uint_as_float(w & 0xffff0000u));
+              };
+              const f32x4 s0 = swap_rows(v0[0], v1[0], v0[1], v1[1]), s1 = swap_rows(v0[2], v1[2], v0[3], v1[3]);
+              const u32x4 w = old[i][hq][0];
+              o = u32x4{add(w[0], s0[0], s0[2]), add(w[1], s1[0], s1[2]), add(w[2], s0[1], s0[3]), add(w[3], s1[1], s1[3])};
+            } else {
+              const f32x4 s = swap_rows(__uint_as_float(pack_bf16x2(v0[0], v0[1])), __uint_as_float(pack_bf16x2(v1[0], v1[1])),
+                                        __uint_as_float(pack_bf16x2(v0[2], v0[3])), __uint_as_float(pack_bf16x2(v1[2], v1[3])));
+              const u32x4 w = __builtin_bit_cast(u32x4, s);
+              o = u32x4{w[0], w[2], w[1], w[3]};
+            }
+            __builtin_amdgcn_raw_buffer_store_b128(o, rd, at, 0, 0);
           }
         }
       }
     }
+    float zero = 0.0f;  // in a vector register: as constants, 128 scalar ones are taken for it
+    asm volatile("" : "+v"(zero));
 #pragma unroll
     for (int hp = 0; hp < 2; ++hp)
 #pragma unroll
@@ -352,12 +422,19 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) acc[hp][hq][i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          for (int j = 0; j < 2; ++j) acc[hp][hq][i][j] = f32x4{zero, zero, zero, zero};
   };
 
   // ======== the stream ========
   int ck = 0;
   bool more = true;
+  // Vector memory instructions complete in the order of issue.  Stores of an
+  // epilogue (2 halves * 4 blocks * 2 * (2 in fp32)) stand between the loads
+  // that a wait is for and itself for one step and a half: `fresh` is 2 in the
+  // step behind one, 1 in the next.  63 is the counter's limit.
+  constexpr int kStores = F32 ? 32 : 16;
+  constexpr int kW1 = 10 + kStores < 63 ? 10 + kStores : 63, kW2 = 8 + kStores < 63 ? 8 + kStores : 63;
+  int fresh = 0;
   // One step from stage S, starting with Q's half S.  Each wait is for loads
   // whose data is read one phase later: the barrier behind it makes them
   // visible to both groups before the first one reads.
@@ -373,7 +450,9 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
     read_q(qs, 1 - S);
     load_p(ps0, 0);
     wait_lds();
-    wait_vm<10>();  // P half 1 of this step
+    fence();
+    if (fresh) wait_vm<kW1>();  // P half 1 of this step
+    else wait_vm<10>();
     barrier();
     mma(0, 1 - S);
     barrier();
@@ -381,7 +460,10 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
     read_p(ps1);
     load_q(qs);
     wait_lds();
-    wait_vm<8>();  // Q and P half 0 of the next step
+    fence();
+    if (fresh == 2) wait_vm<kW2>();  // Q and P half 0 of the next step
+    else wait_vm<8>();
+    fresh = fresh == 2 ? 1 : 0;
     barrier();
     mma(1, 1 - S);
     barrier();
@@ -395,9 +477,13 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
     if (++ck == ct.steps) {
       fence();
       epilogue();
+      fence();
+      fresh = 2;
       ck = 0;
       cpos += stride;
       more = fetch(cpos, ccur, ct);
+      // no tile left: a step may follow (the loop runs two), and stores nothing
+      if (!more) ct.steps = 0;
     }
     barrier();
   };
@@ -417,8 +503,9 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
   barrier();
   if (wm == 1) __builtin_amdgcn_s_barrier();  // half a phase behind
   for (;;) {
+    // Leaving in the middle of the pair would cost a step less at the end of a
+    // workgroup, but the compiler then waits for stage 1 before reading stage 0.
     step(p00, p10, q0, q1, 0);
-    if (!more) break;
     step(p01, p11, q1, q0, 1);
     if (!more) break;
   }

@@ -25,6 +25,7 @@
 //   - The loop is one stream of steps over all of a workgroup's tiles: the loads
 //     cross into the next tile while the current one is finished.
 #include <mutex>
+#include <type_traits>
 
 #include "common.h"
 #include "gemm_runs.h"
@@ -74,7 +75,8 @@ __device__ __forceinline__ void wait_lds() {
 struct Tile {
   int64_t row;  // dgrad: first row; wgrad: first row of the expert
   int rows;     // dgrad: rows of the tile; wgrad: rows of the expert
-  int id, pt, qt, steps;
+  int id, pt, qt;
+  int steps;    // of 64 of the reduction, an even number
 };
 
 // No more than `bytes` from base: reads behind them give zeros, writes are dropped.
@@ -165,7 +167,7 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
         t.id = e;
         t.qt = r / gs;
         t.pt = p0 + r - t.qt * gs;
-        t.steps = n > 0 ? static_cast<int>((n + kStep - 1) / kStep) : 1;
+        t.steps = n > 0 ? static_cast<int>((n + 2 * kStep - 1) / (2 * kStep)) * 2 : 2;
         return true;
       } else {
         const runs::Tile r = runs::decode<16>(table, NR, c, at, fresh_copy(ntk));
@@ -341,7 +343,7 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
   // Stores of the finished tile, then zero accumulators.  Every wavefront
   // issues the same number of them whatever its tile holds (rows and columns
   // outside fall outside the buffer and are dropped), so that the waits of the
-  // next steps can count them.
+  // next two steps can count them.
   auto epilogue = [&]() __attribute__((always_inline)) {
     constexpr int ES = F32 ? 4 : 2;
     const int K = fresh_copy(a.K), N = fresh_copy(a.N);
@@ -426,19 +428,17 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
   };
 
   // ======== the stream ========
-  int ck = 0;
-  bool more = true;
-  // Vector memory instructions complete in the order of issue.  Stores of an
-  // epilogue (2 halves * 4 blocks * 2 * (2 in fp32)) stand between the loads
-  // that a wait is for and itself for one step and a half: `fresh` is 2 in the
-  // step behind one, 1 in the next.  63 is the counter's limit.
-  constexpr int kStores = F32 ? 32 : 16;
-  constexpr int kW1 = 10 + kStores < 63 ? 10 + kStores : 63, kW2 = 8 + kStores < 63 ? 8 + kStores : 63;
-  int fresh = 0;
-  // One step from stage S, starting with Q's half S.  Each wait is for loads
+  // Vector memory instructions complete in the order of issue, so a wait for
+  // loads counts what was issued behind them; in the two steps behind an
+  // epilogue its stores too (63 is the counter's limit).  Each wait is for loads
   // whose data is read one phase later: the barrier behind it makes them
   // visible to both groups before the first one reads.
-  auto step = [&](uint8_t* ps0, uint8_t* ps1, uint8_t* qs, uint8_t* qn, int S) __attribute__((always_inline)) {
+  constexpr int kStores = F32 ? 32 : 16;
+  constexpr int kW1 = 10 + kStores < 63 ? 10 + kStores : 63, kW2 = 8 + kStores < 63 ? 8 + kStores : 63;
+  // One step from stage S, starting with Q's half S.
+  auto step = [&](uint8_t* ps0, uint8_t* ps1, uint8_t* qs, uint8_t* qn, auto S_, auto first_) __attribute__((always_inline)) {
+    constexpr int S = decltype(S_)::value;
+    constexpr bool first = decltype(first_)::value;
     // phase 0
     hold();
     read_p(ps0);
@@ -451,8 +451,7 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
     load_p(ps0, 0);
     wait_lds();
     fence();
-    if (fresh) wait_vm<kW1>();  // P half 1 of this step
-    else wait_vm<10>();
+    wait_vm<first ? kW1 : 10>();  // P half 1 of this step
     barrier();
     mma(0, 1 - S);
     barrier();
@@ -461,9 +460,7 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
     load_q(qs);
     wait_lds();
     fence();
-    if (fresh == 2) wait_vm<kW2>();  // Q and P half 0 of the next step
-    else wait_vm<8>();
-    fresh = fresh == 2 ? 1 : 0;
+    wait_vm<first && S == 0 ? kW2 : 8>();  // Q and P half 0 of the next step
     barrier();
     mma(1, 1 - S);
     barrier();
@@ -474,18 +471,13 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
     wait_lds();
     barrier();
     mma(1, S);
-    if (++ck == ct.steps) {
-      fence();
-      epilogue();
-      fence();
-      fresh = 2;
-      ck = 0;
-      cpos += stride;
-      more = fetch(cpos, ccur, ct);
-      // no tile left: a step may follow (the loop runs two), and stores nothing
-      if (!more) ct.steps = 0;
-    }
     barrier();
+  };
+  using std::integral_constant;
+  // A tile is a whole number of pairs of steps, one from each stage.
+  auto steps = [&](auto first) __attribute__((always_inline)) {
+    step(p00, p10, q0, q1, integral_constant<int, 0>(), first);
+    step(p01, p11, q1, q0, integral_constant<int, 1>(), first);
   };
 
   load_p(p00, 0);
@@ -496,18 +488,21 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
   load_q(q1);
   load_p(p11, 1);
   advance();
-  wait_vm<8>();
+  fence();
+  wait_vm<0>();  // both steps: the first tile has no stores before it to count
   barrier();
   read_q(q0, 0);
   wait_lds();
   barrier();
   if (wm == 1) __builtin_amdgcn_s_barrier();  // half a phase behind
   for (;;) {
-    // Leaving in the middle of the pair would cost a step less at the end of a
-    // workgroup, but the compiler then waits for stage 1 before reading stage 0.
-    step(p00, p10, q0, q1, 0);
-    step(p01, p11, q1, q0, 1);
-    if (!more) break;
+    steps(integral_constant<bool, true>());
+    for (int s = 2; s < ct.steps; s += 2) steps(integral_constant<bool, false>());
+    fence();
+    epilogue();
+    fence();
+    cpos += stride;
+    if (!fetch(cpos, ccur, ct)) break;
   }
   if (wm == 0) __builtin_amdgcn_s_barrier();
   wait_vm<0>();  // the loads behind the last step

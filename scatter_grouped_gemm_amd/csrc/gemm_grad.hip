@@ -42,6 +42,7 @@ typedef __attribute__((ext_vector_type(8))) short s16x8;
 constexpr int kThreads = 512;
 constexpr int kTileN = 256;
 constexpr int kStep = 64;   // of the reduction
+constexpr int kMaxG = 1024;
 constexpr int kGroupN = 8;  // wgrad: tiles along N of a block of the tile order
 
 struct GradArgs {
@@ -100,10 +101,11 @@ __device__ __forceinline__ f32x4 swap_rows(float a, float b, float c, float d) {
   return f32x4{__uint_as_float(r[0]), __uint_as_float(r[1]), __uint_as_float(q[0]), __uint_as_float(q[1])};
 }
 
-// An int that no kernel writes, through the scalar cache: a vector load would
-// make the wavefront wait for all its loads to LDS.
-__device__ __forceinline__ int scalar_load(const int32_t* p) {
-  return *(const __attribute__((address_space(4))) int32_t*)(reinterpret_cast<uintptr_t>(p));
+// Hand-written as the run table's read in gemm_runs.h, for its reason.
+__device__ __forceinline__ int2 lds_read_range(const int2* t) {
+  int2 v;
+  asm volatile("ds_read_b64 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=v"(v) : "v"(runs::lds_off(t)) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ s16x4 read_tr(const uint8_t* p) {
@@ -118,7 +120,7 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
   // knows which loads to LDS a read can depend on.
   __shared__ __attribute__((aligned(1024))) uint8_t p00[16384], p01[16384], p10[16384], p11[16384];
   __shared__ __attribute__((aligned(1024))) uint8_t q0[32768], q1[32768];
-  __shared__ int4 table[WGRAD ? 1 : runs::kTable];
+  __shared__ int4 table[WGRAD ? kMaxG / 2 : runs::kTable];  // wgrad: (first row, rows) of each expert
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -137,6 +139,14 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
     pos = static_cast<int>(blockIdx.x >> 3);
     pos_end = a.G * per;
     stride = static_cast<int>(gridDim.x >> 3);
+    int2* const range = reinterpret_cast<int2*>(table);
+    for (int e = threadIdx.x; e < a.G; e += kThreads) {
+      int64_t s = a.starts[e], n = a.counts[e];
+      if (s < 0 || s > a.M || n < 0) s = 0, n = 0;
+      n = n < a.M - s ? n : a.M - s;
+      range[e] = make_int2(static_cast<int>(s), static_cast<int>(n));
+    }
+    __syncthreads();
   } else {
     runs::Share sh;
     static_assert(runs::kMaxBlocks * 4 <= 32768, "the set-up arrays fit in the stages");
@@ -155,19 +165,18 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
         const int per_ = fresh_copy(per), ntk_ = fresh_copy(ntk), ntn_ = fresh_copy(ntn);
         const int e = at / per_, i = xcd * per_ + (at - e * per_);
         if (i >= ntn_ * ntk_) continue;
-        int64_t s = scalar_load(a.starts + e), n = scalar_load(a.counts + e);
-        if (s < 0 || s > a.M || n < 0) s = 0, n = 0;
-        n = n < a.M - s ? n : a.M - s;
+        const int2 range = lds_read_range(reinterpret_cast<const int2*>(table) + e);
+        const int n = __builtin_amdgcn_readfirstlane(range.y);
         if (ACC && n == 0) continue;
         const int grp = i / (kGroupN * ntk_), p0 = grp * kGroupN;
         const int gs = ntn_ - p0 < kGroupN ? ntn_ - p0 : kGroupN;
         const int r = i - p0 * ntk_;
-        t.row = s;
-        t.rows = static_cast<int>(n);
+        t.row = __builtin_amdgcn_readfirstlane(range.x);
+        t.rows = n;
         t.id = e;
         t.qt = r / gs;
         t.pt = p0 + r - t.qt * gs;
-        t.steps = n > 0 ? static_cast<int>((n + 2 * kStep - 1) / (2 * kStep)) * 2 : 2;
+        t.steps = n > 0 ? (n + 2 * kStep - 1) / (2 * kStep) * 2 : 2;
         return true;
       } else {
         const runs::Tile r = runs::decode<16>(table, NR, c, at, fresh_copy(ntk));
@@ -185,8 +194,10 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
   };
   Tile lt;  // load side
   if (!fetch(pos, cur, lt)) return;
-  Tile ct = lt;  // compute side
-  int cpos = pos, ccur = cur;
+  // Compute side: it is two steps behind the load side, a tile has at least two,
+  // so its next tile is the load side's or the one before that.
+  Tile ct = lt, before = lt;
+  int ahead = 0;  // tiles between the two
 
   // ======== load side ========
   // offsets of this lane's 16 bytes within a step of the operand; a load fills
@@ -260,7 +271,9 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
       Tile t = lt;
       if (fetch(next, cur, t)) {
         pos = next;
+        before = lt;
         lt = t;
+        ++ahead;
         lk = 0;
         lset();
       } else {
@@ -501,8 +514,8 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
     fence();
     epilogue();
     fence();
-    cpos += stride;
-    if (!fetch(cpos, ccur, ct)) break;
+    if (ahead == 0) break;
+    ct = --ahead == 0 ? lt : before;
   }
   if (wm == 0) __builtin_amdgcn_s_barrier();
   wait_vm<0>();  // the loads behind the last step
@@ -516,7 +529,7 @@ int32_t check_sizes(int64_t M, int32_t N, int32_t K, int32_t G) {
   if (N % 128 != 0 || K % 128 != 0) return MOE_EUNSUPPORTED;
   // 256 rows of an operand are addressed with 32-bit offsets
   if (N > (1 << 22) || K > (1 << 22)) return MOE_EUNSUPPORTED;
-  if ((M + 127) / 128 > runs::kMaxBlocks || G > 1024) return MOE_EUNSUPPORTED;
+  if ((M + 127) / 128 > runs::kMaxBlocks || G > kMaxG) return MOE_EUNSUPPORTED;
   // tile positions
   if (((static_cast<int64_t>(N) + 255) / 256) * ((K + 255) / 256) / 8 * G >= (1 << 30)) return MOE_EUNSUPPORTED;
   if ((static_cast<int64_t>(K) + 255) / 256 * ((M + 127) / 128) >= (1 << 30)) return MOE_EUNSUPPORTED;

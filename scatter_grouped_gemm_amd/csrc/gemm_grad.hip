@@ -101,6 +101,17 @@ __device__ __forceinline__ f32x4 swap_rows(float a, float b, float c, float d) {
   return f32x4{__uint_as_float(r[0]), __uint_as_float(r[1]), __uint_as_float(q[0]), __uint_as_float(q[1])};
 }
 
+// The lanes 8 .. 15 of each 16 take b of the lanes 0 .. 7 for a, and these take
+// a of the lanes 8 .. 15 for b.  Done twice, everything is where it was.
+__device__ __forceinline__ void trade8(u32x4& a, u32x4& b) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t x = a[e], y = b[e];
+    a[e] = __builtin_amdgcn_update_dpp(x, y, 0x128 /* row_ror:8 */, 0xf, 0xc, false);
+    b[e] = __builtin_amdgcn_update_dpp(y, x, 0x128, 0xf, 0x3, false);
+  }
+}
+
 // Hand-written as the run table's read in gemm_runs.h, for its reason.
 __device__ __forceinline__ int2 lds_read_range(const int2* t) {
   int2 v;
@@ -366,11 +377,16 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
     int l = lane;
     asm volatile("" : "+v"(l));
     const int row = l & 15, g = l >> 4;
-    // fp32: four consecutive columns of each 16-column block.  bf16: eight, of
-    // block 0 in even lane groups and of block 1 in odd ones (see below).
-    const int col = F32 ? g * 4 : (g & 1) * 16 + (g >> 1) * 8;
+    // A store of a wavefront covers eight rows and a whole 128-byte line of
+    // each (16 rows of half a line take the texture unit longer).  A lane's
+    // accumulators are four columns of row `row` in each 16-column block, so
+    // lanes trade: bf16, first with the lane 16 on (swap_rows: eight columns in
+    // a row, of block 0 in even lane groups and of block 1 in odd ones); then the
+    // lanes 0 .. 7 of each 16 give the second half of their line for the first
+    // half of the row eight on (trade8).
+    const int col = F32 ? g * 4 + (row >> 3) * 16 : (g & 1) * 16 + (g >> 1) * 8 + (row >> 3) * 32;
     const int line = K * ES;  // 64 rows of it are at most 2^30 bytes
-    const uint32_t off = row * line + col * ES;
+    const uint32_t off = (row & 7) * line + col * ES;
 #pragma unroll
     for (int hp = 0; hp < 2; ++hp) {
       const int r0 = hp * 128 + wm * 64;  // of the tile
@@ -379,52 +395,56 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
       rows = rows < 64 ? rows : 64;
       const int bytes = col0 < K && rows > 0 ? rows * line - col0 * ES : 0;
       const auto rd = buffer(static_cast<uint8_t*>(a.D) + first * line + col0 * ES, bytes);
-      constexpr int NJ = F32 ? 2 : 1;  // 16-byte accesses of 32 columns
-      u32x4 old[4][2][NJ];
+      constexpr int NQ = F32 ? 2 : 1;  // lines of a row
+      u32x4 old[4][NQ][2];
       if constexpr (ACC) {  // all of a half in flight together
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int hq = 0; hq < 2; ++hq)
+          for (int q = 0; q < NQ; ++q)
 #pragma unroll
-            for (int j = 0; j < NJ; ++j)
-              old[i][hq][j] = __builtin_amdgcn_raw_buffer_load_b128(rd, off + i * 16 * line + hq * 32 * ES + j * 64, 0, 0);
+            for (int h = 0; h < 2; ++h)
+              old[i][q][h] = __builtin_amdgcn_raw_buffer_load_b128(rd, off + (i * 16 + h * 8) * line + q * 128, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        const uint32_t at = off + i * 16 * line;
 #pragma unroll
-        for (int hq = 0; hq < 2; ++hq) {
-          const uint32_t at = off + i * 16 * line + hq * 32 * ES;
-          f32x4 v0 = acc[hp][hq][i][0], v1 = acc[hp][hq][i][1];
+        for (int q = 0; q < NQ; ++q) {
+          u32x4 w[2];
+          if constexpr (ACC) trade8(old[i][q][0], old[i][q][1]);
           if constexpr (F32) {
-            if constexpr (ACC) {
-              v0 += __builtin_bit_cast(f32x4, old[i][hq][0]);
-              v1 += __builtin_bit_cast(f32x4, old[i][hq][NJ - 1]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              f32x4 v = acc[hp][q][i][j];
+              if constexpr (ACC) v += __builtin_bit_cast(f32x4, old[i][q][j]);
+              w[j] = __builtin_bit_cast(u32x4, v);
             }
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v0), rd, at, 0, 0);
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v1), rd, at + 64, 0, 0);
           } else {
-            // Lanes of an odd group swap their part of block 0 for the part of
-            // block 1 that the group before them holds: eight columns in a row
-            // for one 16-byte access.  Where the old value has to be added,
-            // this is done in fp32, so that the sum is rounded once.
-            u32x4 o;
-            if constexpr (ACC) {
-              const auto add = [&](uint32_t w, float lo, float hi) __attribute__((always_inline)) {
-                return pack_bf16x2(lo + __uint_as_float(w << 16), hi + __uint_as_float(w & 0xffff0000u));
-              };
-              const f32x4 s0 = swap_rows(v0[0], v1[0], v0[1], v1[1]), s1 = swap_rows(v0[2], v1[2], v0[3], v1[3]);
-              const u32x4 w = old[i][hq][0];
-              o = u32x4{add(w[0], s0[0], s0[2]), add(w[1], s1[0], s1[2]), add(w[2], s0[1], s0[3]), add(w[3], s1[1], s1[3])};
-            } else {
-              const f32x4 s = swap_rows(__uint_as_float(pack_bf16x2(v0[0], v0[1])), __uint_as_float(pack_bf16x2(v1[0], v1[1])),
-                                        __uint_as_float(pack_bf16x2(v0[2], v0[3])), __uint_as_float(pack_bf16x2(v1[2], v1[3])));
-              const u32x4 w = __builtin_bit_cast(u32x4, s);
-              o = u32x4{w[0], w[2], w[1], w[3]};
+#pragma unroll
+            for (int hq = 0; hq < 2; ++hq) {
+              const f32x4 v0 = acc[hp][hq][i][0], v1 = acc[hp][hq][i][1];
+              if constexpr (ACC) {
+                // added in fp32, so that the sum is rounded once
+                const auto add = [&](uint32_t o, float lo, float hi) __attribute__((always_inline)) {
+                  return pack_bf16x2(lo + __uint_as_float(o << 16), hi + __uint_as_float(o & 0xffff0000u));
+                };
+                const f32x4 s0 = swap_rows(v0[0], v1[0], v0[1], v1[1]), s1 = swap_rows(v0[2], v1[2], v0[3], v1[3]);
+                const u32x4 o = old[i][0][hq];
+                w[hq] = u32x4{add(o[0], s0[0], s0[2]), add(o[1], s1[0], s1[2]), add(o[2], s0[1], s0[3]), add(o[3], s1[1], s1[3])};
+              } else {
+                const u32x4 o = __builtin_bit_cast(
+                    u32x4, swap_rows(__uint_as_float(pack_bf16x2(v0[0], v0[1])), __uint_as_float(pack_bf16x2(v1[0], v1[1])),
+                                     __uint_as_float(pack_bf16x2(v0[2], v0[3])), __uint_as_float(pack_bf16x2(v1[2], v1[3]))));
+                w[hq] = u32x4{o[0], o[2], o[1], o[3]};
+              }
             }
-            __builtin_amdgcn_raw_buffer_store_b128(o, rd, at, 0, 0);
           }
+          trade8(w[0], w[1]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            __builtin_amdgcn_raw_buffer_store_b128(w[h], rd, at + h * 8 * line + q * 128, 0, 0);
         }
       }
     }

@@ -29,6 +29,7 @@
 
 #include "common.h"
 #include "gemm_runs.h"
+#include "grad_schedule.h"
 
 namespace moe {
 namespace {
@@ -42,7 +43,6 @@ typedef __attribute__((ext_vector_type(8))) short s16x8;
 constexpr int kThreads = 512;
 constexpr int kTileN = 256;
 constexpr int kStep = 64;   // of the reduction
-constexpr int kMaxG = 1024;
 constexpr int kGroupN = 8;  // wgrad: tiles along N of a block of the tile order
 
 struct GradArgs {
@@ -57,6 +57,7 @@ struct GradArgs {
 };
 
 using runs::wait_vm;
+using sched::kMaxG;
 
 __device__ __forceinline__ void fence() {
   __builtin_amdgcn_sched_barrier(0);
@@ -112,13 +113,6 @@ __device__ __forceinline__ void trade8(u32x4& a, u32x4& b) {
   }
 }
 
-// Hand-written as the run table's read in gemm_runs.h, for its reason.
-__device__ __forceinline__ int2 lds_read_range(const int2* t) {
-  int2 v;
-  asm volatile("ds_read_b64 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=v"(v) : "v"(runs::lds_off(t)) : "memory");
-  return v;
-}
-
 __device__ __forceinline__ s16x4 read_tr(const uint8_t* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
       (__attribute__((address_space(3))) s16x4*)(p));
@@ -131,7 +125,8 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
   // knows which loads to LDS a read can depend on.
   __shared__ __attribute__((aligned(1024))) uint8_t p00[16384], p01[16384], p10[16384], p11[16384];
   __shared__ __attribute__((aligned(1024))) uint8_t q0[32768], q1[32768];
-  __shared__ int4 table[WGRAD ? kMaxG / 2 : runs::kTable];  // wgrad: (first row, rows) of each expert
+  __shared__ int4 table[WGRAD ? 1 : runs::kTable];
+  __shared__ typename std::conditional<WGRAD, sched::Lds, int>::type dealt;
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -141,70 +136,58 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
   const int ntk = (a.K + kTileN - 1) / kTileN;
 
   // ======== the tiles of this workgroup ========
-  int pos, pos_end, stride, per = 0, ntn = 0;
-  int NR = 0, cur = 0;
-  const int xcd = blockIdx.x & 7;
+  int pos = 0, pos_end = 0, stride = 0, NR = 0, cur = 0;
+  [[maybe_unused]] sched::Dealer dealer;
+  const int ntn = (a.N + kTileN - 1) / kTileN;
   if constexpr (WGRAD) {
-    ntn = (a.N + kTileN - 1) / kTileN;
-    per = (ntn * ntk + 7) / 8;  // of each expert, for this XCD
-    pos = static_cast<int>(blockIdx.x >> 3);
-    pos_end = a.G * per;
-    stride = static_cast<int>(gridDim.x >> 3);
-    int2* const range = reinterpret_cast<int2*>(table);
-    for (int e = threadIdx.x; e < a.G; e += kThreads) {
-      int64_t s = a.starts[e], n = a.counts[e];
-      if (s < 0 || s > a.M || n < 0) s = 0, n = 0;
-      n = n < a.M - s ? n : a.M - s;
-      range[e] = make_int2(static_cast<int>(s), static_cast<int>(n));
-    }
-    __syncthreads();
+    sched::deal<8>(dealer, &dealt, reinterpret_cast<int2*>(q0), a.starts, a.counts, a.M, a.G, ntn * ntk, kStep, ACC);
   } else {
     runs::Share sh;
     static_assert(runs::kMaxBlocks * 4 <= 32768, "the set-up arrays fit in the stages");
     if (!runs::build_share<8>(a.m_indices, a.M, a.G, ntk, reinterpret_cast<int*>(q0),
                               reinterpret_cast<int*>(q1), reinterpret_cast<int*>(p00), table, sh))
       return;
-    NR = sh.NR;
-    pos = sh.lo + static_cast<int>(blockIdx.x >> 3);
-    pos_end = sh.hi;
+    NR = sched::uniform(sh.NR);
+    pos = sched::uniform(sh.lo) + static_cast<int>(blockIdx.x >> 3);
+    pos_end = sched::uniform(sh.hi);
     stride = sh.per_xcd;
   }
-  // The tile at pos or the next one with work; false: none left.
-  auto fetch = [&](int& at, int& c, Tile& t) __attribute__((always_inline)) -> bool {
-    for (; at < pos_end; at += stride) {
-      if constexpr (WGRAD) {
-        const int per_ = fresh_copy(per), ntk_ = fresh_copy(ntk), ntn_ = fresh_copy(ntn);
-        const int e = at / per_, i = xcd * per_ + (at - e * per_);
-        if (i >= ntn_ * ntk_) continue;
-        const int2 range = lds_read_range(reinterpret_cast<const int2*>(table) + e);
-        const int n = __builtin_amdgcn_readfirstlane(range.y);
-        if (ACC && n == 0) continue;
-        const int grp = i / (kGroupN * ntk_), p0 = grp * kGroupN;
-        const int gs = ntn_ - p0 < kGroupN ? ntn_ - p0 : kGroupN;
-        const int r = i - p0 * ntk_;
-        t.row = __builtin_amdgcn_readfirstlane(range.x);
-        t.rows = n;
-        t.id = e;
-        t.qt = r / gs;
-        t.pt = p0 + r - t.qt * gs;
-        t.steps = n > 0 ? (n + 2 * kStep - 1) / (2 * kStep) * 2 : 2;
-        return true;
-      } else {
-        const runs::Tile r = runs::decode<16>(table, NR, c, at, fresh_copy(ntk));
-        if (r.rows <= 0) continue;
-        t.row = r.row;
-        t.rows = r.rows;
-        t.id = r.id;
-        t.pt = 0;
-        t.qt = r.nt;
-        t.steps = a.N / kStep;
-        return true;
-      }
+  // The workgroup's next tile; false: none left.
+  auto fetch = [&](Tile& t) __attribute__((always_inline)) -> bool {
+    if constexpr (WGRAD) {
+      int s, i;
+      if (!sched::next(dealer, s, i)) return false;
+      const int ntk_ = fresh_copy(ntk), ntn_ = fresh_copy(ntn);
+      const int2 range = sched::lds_int2(&dealt.range[s]);
+      const int grp = i / (kGroupN * ntk_), p0 = grp * kGroupN;
+      const int gs = ntn_ - p0 < kGroupN ? ntn_ - p0 : kGroupN;
+      const int r = i - p0 * ntk_;
+      t.row = sched::uniform(range.x);
+      t.rows = sched::uniform(range.y);
+      t.id = sched::uniform(sched::lds_int(&dealt.id[s]));
+      t.qt = r / gs;
+      t.pt = p0 + r - t.qt * gs;
+      t.steps = sched::tile_steps(t.rows, kStep);
+      return true;
+    } else {
+      int at = pos, c = cur;
+      runs::Tile r;
+      r.rows = 0;
+      for (; at < pos_end && r.rows <= 0; at += stride) r = runs::decode<16>(table, NR, c, at, fresh_copy(ntk));
+      if (r.rows <= 0) return false;
+      pos = at;
+      cur = c;
+      t.row = r.row;
+      t.rows = r.rows;
+      t.id = r.id;
+      t.pt = 0;
+      t.qt = r.nt;
+      t.steps = a.N / kStep;
+      return true;
     }
-    return false;
   };
   Tile lt;  // load side
-  if (!fetch(pos, cur, lt)) return;
+  if (!fetch(lt)) return;
   // Compute side: it is two steps behind the load side, a tile has at least two,
   // so its next tile is the load side's or the one before that.
   Tile ct = lt, before = lt;
@@ -278,10 +261,8 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
   // never used), so that every step issues the same loads
   auto advance = [&]() __attribute__((always_inline)) {
     if (++lk == lt.steps) {
-      int next = pos + stride;
       Tile t = lt;
-      if (fetch(next, cur, t)) {
-        pos = next;
+      if (fetch(t)) {
         before = lt;
         lt = t;
         ++ahead;
@@ -565,7 +546,7 @@ int grid_size() {
   std::call_once(once[dev], [dev]() {
     int cus = 0;
     if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess)
-      grid[dev] = cus >= 8 ? cus / 8 * 8 : 8;
+      grid[dev] = cus < 8 ? 8 : cus / 8 > sched::kMaxP ? 8 * sched::kMaxP : cus / 8 * 8;
   });
   return grid[dev];
 }

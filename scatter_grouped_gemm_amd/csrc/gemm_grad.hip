@@ -138,9 +138,11 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
   // ======== the tiles of this workgroup ========
   int pos = 0, pos_end = 0, stride = 0, NR = 0, cur = 0;
   [[maybe_unused]] sched::Dealer dealer;
+  // of a tile's start and stores, in steps of the reduction
+  constexpr int kTileCost = (F32 ? 8 : 4) * (ACC ? 2 : 1);
   const int ntn = (a.N + kTileN - 1) / kTileN;
   if constexpr (WGRAD) {
-    sched::deal<8>(dealer, &dealt, reinterpret_cast<int2*>(q0), a.starts, a.counts, a.M, a.G, ntn * ntk, kStep, ACC);
+    sched::deal<8>(dealer, &dealt, reinterpret_cast<int2*>(q0), a.starts, a.counts, a.M, a.G, ntn * ntk, kStep, kTileCost, ACC);
   } else {
     runs::Share sh;
     static_assert(runs::kMaxBlocks * 4 <= 32768, "the set-up arrays fit in the stages");
@@ -512,9 +514,14 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
   for (;;) {
     steps(integral_constant<bool, true>());
     for (int s = 2; s < ct.steps; s += 2) steps(integral_constant<bool, false>());
+    // Accumulating, both groups do this at the same time to have twice the loads
+    // in flight: the first one waits for the second one's MFMAs, the second one
+    // falls back by half a phase again behind it.
+    if (ACC && wm == 0) barrier();
     fence();
     epilogue();
     fence();
+    if (ACC && wm == 1) barrier();
     if (ahead == 0) break;
     ct = --ahead == 0 ? lt : before;
   }

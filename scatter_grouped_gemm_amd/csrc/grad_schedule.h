@@ -28,7 +28,6 @@ namespace sched {
 
 constexpr int kMaxG = 1024;
 constexpr int kMaxP = 64;       // workgroups of an XCD
-constexpr int kTileCost = 4;    // of a tile's start and stores, in steps
 
 struct Lds {
   int2 range[kMaxG];            // (first row, rows), rows falling
@@ -72,11 +71,11 @@ struct Dealer {
 };
 
 // Sets up the dealing: all 64 * WAVES threads call it, `raw` is kMaxG int2 of LDS
-// to work in.  skip_empty: experts without rows have no tiles.
+// to work in.  A tile costs its steps and tile_cost.  skip_empty: experts without rows have no tiles.
 template <int WAVES>
 __device__ __forceinline__ void deal(Dealer& d, Lds* L, int2* raw, const int32_t* __restrict__ starts,
                                      const int32_t* __restrict__ counts, int64_t M, int G, int tiles,
-                                     int step, bool skip_empty) {
+                                     int step, int tile_cost, bool skip_empty) {
   constexpr int kThreads = 64 * WAVES;
   static_assert(2 * kThreads >= kMaxG && kThreads >= kMaxP + 1, "a thread has two experts");
   const int tid = threadIdx.x;
@@ -109,7 +108,7 @@ __device__ __forceinline__ void deal(Dealer& d, Lds* L, int2* raw, const int32_t
   for (int i = 0; i < 2; ++i) {
     const int s = 2 * tid + i;
     r[i] = s < d.G ? share(s, xcd, tiles).y % P : 0;
-    c[i] = r[i] > 0 ? r[i] * (tile_steps(L->range[s].y, step) + kTileCost) : 0;
+    c[i] = r[i] > 0 ? r[i] * (tile_steps(L->range[s].y, step) + tile_cost) : 0;
   }
   const int2 base = runs::scan_excl_sum2<WAVES>(r[0] + r[1], c[0] + c[1], L->scr, tot);
   if (2 * tid < kMaxG) {
@@ -136,7 +135,7 @@ __device__ __forceinline__ void deal(Dealer& d, Lds* L, int2* raw, const int32_t
   if (tid < 64) {
     const int b = tid;
     int load = 0;
-    if (b < P && b < tot.x) load = tile_steps(L->range[last(L->items, b)].y, step) + kTileCost;
+    if (b < P && b < tot.x) load = tile_steps(L->range[last(L->items, b)].y, step) + tile_cost;
     int sum = load;  // of the workgroups from b on (smaller items)
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -150,7 +149,7 @@ __device__ __forceinline__ void deal(Dealer& d, Lds* L, int2* raw, const int32_t
       int t = tot.x;
       if (x < tot.y) {
         const int s = last(L->cost, x);
-        const int each = tile_steps(L->range[s].y, step) + kTileCost;
+        const int each = tile_steps(L->range[s].y, step) + tile_cost;
         t = L->items[s] + (x - L->cost[s] + each - 1) / each;
       }
       t = t < tot.x ? t : tot.x;

@@ -337,16 +337,29 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _dev(name: str, dtype, shape, t) -> int:
+# The current stream of a device without building a Stream object (a third of a
+# small call's time); the public way where torch does not have it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _dev(name: str, dtype, shape, t, dev: int) -> int:
     """Data pointer of an operand of the training calls: a contiguous tensor of
     this dtype and shape on the current device (the stream's)."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name}: want {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{name}: is on {t.device}, not on the current device")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name}: must be contiguous")
+
+
+def _current() -> int:
+    """The current device; -2, which no operand is on, where there is none."""
+    if torch.cuda.is_initialized() or torch.cuda.is_available():
+        return torch.cuda.current_device()
+    return -2
 
 
 _BF16, _F32, _INT32 = torch.bfloat16, torch.float32, torch.int32
@@ -360,10 +373,11 @@ def moe_combine_bwd(dout, Y, src2dst, topk_weights, dY, dtopk_weights):
     k = src2dst.shape[1]
     _need(Y.shape[-1] == H, "moe_combine_bwd: Y and dout differ in width")
     rows = Y.numel() // H if H else 0
+    dev = _current()
     _check("moe_combine_bwd", lib().moe_combine_bwd(
-        _dev("dout", _BF16, (T, H), dout), _dev("Y", _BF16, Y.shape, Y), rows,
-        _dev("src2dst", _INT32, (T, k), src2dst), _dev("topk_weights", _F32, (T, k), topk_weights), T, k, H,
-        _dev("dY", _BF16, Y.shape, dY), _dev("dtopk_weights", _F32, (T, k), dtopk_weights), _stream()))
+        _dev("dout", _BF16, (T, H), dout, dev), _dev("Y", _BF16, Y.shape, Y, dev), rows,
+        _dev("src2dst", _INT32, (T, k), src2dst, dev), _dev("topk_weights", _F32, (T, k), topk_weights, dev), T, k, H,
+        _dev("dY", _BF16, Y.shape, dY, dev), _dev("dtopk_weights", _F32, (T, k), dtopk_weights, dev), _raw_stream(dev)))
 
 
 def moe_route_topk_bwd(topk_ids, topk_weights, dtopk_weights, dlogits):
@@ -371,10 +385,11 @@ def moe_route_topk_bwd(topk_ids, topk_weights, dtopk_weights, dlogits):
     _need(topk_ids.dim() == 2 and dlogits.dim() == 2, "moe_route_topk_bwd: topk_ids and dlogits are matrices")
     T, k = topk_ids.shape
     E = dlogits.shape[1]
+    dev = _current()
     _check("moe_route_topk_bwd", lib().moe_route_topk_bwd(
-        _dev("topk_ids", _INT32, (T, k), topk_ids), _dev("topk_weights", _F32, (T, k), topk_weights),
-        _dev("dtopk_weights", _F32, (T, k), dtopk_weights), T, E, k,
-        _dev("dlogits", _F32, (T, E), dlogits), _stream()))
+        _dev("topk_ids", _INT32, (T, k), topk_ids, dev), _dev("topk_weights", _F32, (T, k), topk_weights, dev),
+        _dev("dtopk_weights", _F32, (T, k), dtopk_weights, dev), T, E, k,
+        _dev("dlogits", _F32, (T, E), dlogits, dev), _raw_stream(dev)))
 
 
 def moe_scatter_bwd(dX, src2dst, dx):
@@ -384,9 +399,10 @@ def moe_scatter_bwd(dX, src2dst, dx):
     H = dx.shape[1]
     _need(dX.shape[-1] == H, "moe_scatter_bwd: dX and dx differ in width")
     rows = dX.numel() // H if H else 0
+    dev = _current()
     _check("moe_scatter_bwd", lib().moe_scatter_bwd(
-        _dev("dX", _BF16, dX.shape, dX), rows, _dev("src2dst", _INT32, (T, k), src2dst), T, k, H,
-        _dev("dx", _BF16, (T, H), dx), _stream()))
+        _dev("dX", _BF16, dX.shape, dX, dev), rows, _dev("src2dst", _INT32, (T, k), src2dst, dev), T, k, H,
+        _dev("dx", _BF16, (T, H), dx, dev), _raw_stream(dev)))
 
 
 def silu_and_mul_bwd(gateup, dact, dgateup, act=None, m_indices=None, masked_m=None, max_m=0):
@@ -397,12 +413,13 @@ def silu_and_mul_bwd(gateup, dact, dgateup, act=None, m_indices=None, masked_m=N
     I = N // 2
     _need(masked_m is None or (max_m > 0 and masked_m.numel() * max_m == M),
           "silu_and_mul_bwd: masked_m and max_m do not make up M rows")
+    dev = _current()
     _check("silu_and_mul_bwd", lib().silu_and_mul_bwd(
-        _dev("gateup", _BF16, (M, N), gateup), _dev("dact", _BF16, (M, I), dact), M, I,
-        None if m_indices is None else _dev("m_indices", _INT32, (M,), m_indices),
-        None if masked_m is None else _dev("masked_m", _INT32, masked_m.shape, masked_m), max_m,
-        _dev("dgateup", _BF16, (M, N), dgateup),
-        None if act is None else _dev("act", _BF16, (M, I), act), _stream()))
+        _dev("gateup", _BF16, (M, N), gateup, dev), _dev("dact", _BF16, (M, I), dact, dev), M, I,
+        None if m_indices is None else _dev("m_indices", _INT32, (M,), m_indices, dev),
+        None if masked_m is None else _dev("masked_m", _INT32, masked_m.shape, masked_m, dev), max_m,
+        _dev("dgateup", _BF16, (M, N), dgateup, dev),
+        None if act is None else _dev("act", _BF16, (M, I), act, dev), _raw_stream(dev)))
 
 
 def grouped_gemm_contig_dgrad(dC, B, dA, m_indices):
@@ -411,9 +428,10 @@ def grouped_gemm_contig_dgrad(dC, B, dA, m_indices):
     _need(dC.dim() == 2 and B.dim() == 3, "grouped_gemm_contig_dgrad: dC is [M, N] and B [G, N, K]")
     M = dC.shape[0]
     G, N, K = B.shape
+    dev = _current()
     _check("grouped_gemm_contig_dgrad", lib().grouped_gemm_contig_dgrad(
-        _dev("dC", _BF16, (M, N), dC), _dev("B", _BF16, (G, N, K), B), _dev("dA", _BF16, (M, K), dA),
-        _dev("m_indices", _INT32, (M,), m_indices), M, N, K, G, _stream()))
+        _dev("dC", _BF16, (M, N), dC, dev), _dev("B", _BF16, (G, N, K), B, dev), _dev("dA", _BF16, (M, K), dA, dev),
+        _dev("m_indices", _INT32, (M,), m_indices, dev), M, N, K, G, _raw_stream(dev)))
 
 
 def grouped_gemm_contig_wgrad(dC, A, expert_start_loc, num_valid, dB, accumulate=False):
@@ -423,11 +441,12 @@ def grouped_gemm_contig_wgrad(dC, A, expert_start_loc, num_valid, dB, accumulate
     M = dC.shape[0]
     G, N, K = dB.shape
     _need(dB.dtype in (_BF16, _F32), "grouped_gemm_contig_wgrad: dB is bf16 or fp32")
+    dev = _current()
     _check("grouped_gemm_contig_wgrad", lib().grouped_gemm_contig_wgrad(
-        _dev("dC", _BF16, (M, N), dC), _dev("A", _BF16, (M, K), A),
-        _dev("expert_start_loc", _INT32, (G,), expert_start_loc), _dev("num_valid", _INT32, (G,), num_valid),
+        _dev("dC", _BF16, (M, N), dC, dev), _dev("A", _BF16, (M, K), A, dev),
+        _dev("expert_start_loc", _INT32, (G,), expert_start_loc, dev), _dev("num_valid", _INT32, (G,), num_valid, dev),
         MOE_DTYPE_FP32 if dB.dtype is _F32 else MOE_DTYPE_BF16, int(bool(accumulate)),
-        _dev("dB", dB.dtype, (G, N, K), dB), M, N, K, G, _stream()))
+        _dev("dB", dB.dtype, (G, N, K), dB, dev), M, N, K, G, _raw_stream(dev)))
 
 
 def moe_adamw_plan(tensors) -> torch.Tensor:
@@ -441,7 +460,8 @@ def moe_adamw_plan(tensors) -> torch.Tensor:
 
 def moe_adamw_step(plan, lr, counter, beta1, beta2, eps, seed=0, grad_scale=None):
     """One AdamW step over the tensors of a device plan."""
+    dev = _current()
     _check("moe_adamw_step", lib().moe_adamw_step(
-        _dev("plan", torch.uint8, plan.shape, plan), plan.numel(), _dev("lr", _F32, (1,), lr),
-        None if grad_scale is None else _dev("grad_scale", _F32, (1,), grad_scale),
-        _dev("counter", torch.int64, (2,), counter), beta1, beta2, eps, seed & 0xffffffff, _stream()))
+        _dev("plan", torch.uint8, plan.shape, plan, dev), plan.numel(), _dev("lr", _F32, (1,), lr, dev),
+        None if grad_scale is None else _dev("grad_scale", _F32, (1,), grad_scale, dev),
+        _dev("counter", torch.int64, (2,), counter, dev), beta1, beta2, eps, seed & 0xffffffff, _raw_stream(dev)))

@@ -171,6 +171,15 @@ __device__ __forceinline__ void deal(Dealer& d, Lds* L, int2* raw, const int32_t
   d.at = 0;
 }
 
+// Its first item among those that m workgroups take in turn.  The turn goes by the
+// item's number and not by its place among these: they may be one or two only,
+// and would always fall to the same workgroup.
+__device__ __forceinline__ int first_of(const Dealer& d, int rho) {
+  const int from = uniform(lds_int(&d.L->tm[d.m - 1]));
+  const int ahead = rho - (from - d.P) % d.m;
+  return from + (ahead < 0 ? ahead + d.m : ahead);
+}
+
 // The workgroup's next tile: expert s and tile i of it; false: none left.
 __device__ __forceinline__ bool next(Dealer& d, int& s, int& i) {
   while (d.s < d.G) {
@@ -188,7 +197,7 @@ __device__ __forceinline__ bool next(Dealer& d, int& s, int& i) {
   int t;
   if (d.m == 0) {
     d.m = rho + 1;
-    d.t = uniform(lds_int(&d.L->tm[rho])) + rho;
+    d.t = first_of(d, rho);
     t = d.w;
     if (t >= d.total) return false;  // fewer items than workgroups
   } else {
@@ -196,7 +205,7 @@ __device__ __forceinline__ bool next(Dealer& d, int& s, int& i) {
       if (d.m > d.P) return false;
       if (d.t < uniform(lds_int(&d.L->tm[d.m]))) break;
       if (++d.m > d.P) return false;
-      d.t = uniform(lds_int(&d.L->tm[d.m - 1])) + rho;
+      d.t = first_of(d, rho);
     }
     t = d.t;
     d.t += d.m;

@@ -31,7 +31,8 @@ class AdamW:
     written between steps.  ``master``, ``m``, ``v`` (and ``m_scale``,
     ``v_scale``) are flat over all tensors, tensor i at ``offsets[i]``, a
     multiple of 128; ``v`` holds the codes of its root where state_bits is 8.
-    They are what a checkpoint has to keep, with ``steps``.
+    ``state_dict`` gives
+    what a checkpoint has to keep (and the fp32 parameters, which are the caller's).
     """
 
     def __init__(self, params, grads, *, lr: float = 1e-3, betas=(0.9, 0.95), eps: float = 1e-8,
@@ -95,6 +96,29 @@ class AdamW:
         for p, at in zip(self.params, self.offsets):
             if p.dtype is torch.bfloat16:
                 self.master[at:at + p.numel()].copy_(p.reshape(-1))
+
+    def state_dict(self) -> dict:
+        """The state's tensors (not copies): what a checkpoint has to keep."""
+        names = ("master", "m", "v", "m_scale", "v_scale", "lr")
+        return {"steps": self.steps, "offsets": list(self.offsets), "state_bits": self.state_bits,
+                **{n: getattr(self, n) for n in names if getattr(self, n) is not None}}
+
+    def load_state_dict(self, state: dict):
+        """Take over another run's state_dict (same tensors, same state_bits); bf16
+        parameters become their masters' roundings."""
+        mine = self.state_dict()
+        if state["state_bits"] != self.state_bits or list(state["offsets"]) != self.offsets or state.keys() != mine.keys():
+            raise ValueError("the state is of other tensors or another state_bits")
+        for n, t in mine.items():
+            if isinstance(t, torch.Tensor):
+                if state[n].shape != t.shape or state[n].dtype != t.dtype:
+                    raise ValueError(f"{n}: want {t.dtype} {tuple(t.shape)}, got {state[n].dtype} {tuple(state[n].shape)}")
+        for n, t in mine.items():
+            if isinstance(t, torch.Tensor):
+                t.copy_(state[n])
+        for p, at in zip(self.params, self.offsets):
+            if p.dtype is torch.bfloat16:
+                p.copy_(self.master[at:at + p.numel()].view(p.shape))
 
     def step(self, grad_scale: torch.Tensor | None = None):
         """Update every parameter from its gradient, times grad_scale (device fp32 [1]) if given."""

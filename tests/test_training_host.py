@@ -119,6 +119,26 @@ def test_adamw_class_refuses():
     assert torch.equal(o.master[:130], a.float())
 
 
+def test_adamw_state_round_trip_on_host():
+    a, b = torch.randn(130).bfloat16(), torch.randn(7)
+    make = lambda p, q, bits=8: AdamW([p, q], [torch.zeros_like(p), torch.zeros_like(q)], state_bits=bits)  # noqa: E731
+    o = make(a, b)
+    for t in (o.master, o.m, o.v, o.m_scale, o.v_scale, o.steps, o.lr):
+        t.copy_(torch.arange(t.numel()).to(t.dtype))
+    saved = {k: v.clone() if isinstance(v, torch.Tensor) else v for k, v in o.state_dict().items()}
+    c = torch.zeros(130).bfloat16()
+    n = make(c, b)
+    n.load_state_dict(saved)
+    for k, v in saved.items():
+        assert torch.equal(v, n.state_dict()[k]) if isinstance(v, torch.Tensor) else v == n.state_dict()[k]
+    assert torch.equal(c, torch.arange(130).float().bfloat16()) and n._counter[1] == 0
+    for other in (make(a, b, 32), make(b, a)):
+        with pytest.raises(ValueError):
+            other.load_state_dict(saved)
+    with pytest.raises(ValueError):
+        n.load_state_dict({**saved, "m": saved["m"][:128]})
+
+
 def test_wrappers_refuse_host_tensors_types_and_shapes():
     bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
     i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731

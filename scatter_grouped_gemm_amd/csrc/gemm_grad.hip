@@ -530,6 +530,117 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
 #endif
 }
 
+// dgrad with few tiles: 64 rows by 64 columns a workgroup.
+//
+// With few rows the product is one pass over B, and what counts is how many CUs
+// read it and how much each has in flight.  A 256-column tile of a B [8192][2048]
+// leaves 8 workgroups an expert, each reading 4 MB a step at a time: 133 us for
+// one token and two experts, where the bytes take 14.  Here four wavefronts of 16
+// columns each keep seven steps of 64 (56 KB of B) in flight in eight LDS stages
+// of 16 KB.  The sum of an output runs through the same MFMAs in the same order
+// as in the large kernel, so a row comes out the same from either.
+constexpr int kThinStages = 8;
+constexpr int kThinStage = 16384;  // P [64 rows][64], then Q [64][64 columns]
+
+__global__ __launch_bounds__(256, 1) void dgrad_thin_kernel(const GradArgs a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int fr = lane & 15, fg = lane >> 4;
+  const int64_t ldp = static_cast<int64_t>(a.N) * 2, ldq = static_cast<int64_t>(a.K) * 2;
+  const int cols = a.K / 64;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x / cols) * 64;
+  const int col0 = static_cast<int>(blockIdx.x % cols) * 64;
+  // valid rows come first in a block of 128, which has one expert
+  const int e = __builtin_amdgcn_readfirstlane(a.m_indices[row0]);
+  if (e < 0 || e >= a.G) return;
+  const bool valid = row0 + lane < a.M && a.m_indices[row0 + lane] >= 0;
+  const int rows = static_cast<int>(__popcll(__ballot(valid)));
+  const int steps = a.N / kStep;
+
+  uint32_t vp[2], vq[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int r = (wave * 2 + j) * 8 + (lane >> 3);
+    vp[j] = static_cast<uint32_t>(r * ldp) + (((lane & 7) ^ (lane >> 3)) << 4);
+    vq[j] = static_cast<uint32_t>(r * ldq) + ((((lane & 7) >> 1) ^ (r & 3)) << 5) + ((lane & 1) << 4);
+  }
+  const uint8_t* bp = a.P + row0 * ldp;
+  const uint8_t* bq = a.Q + static_cast<int64_t>(e) * a.N * ldq + col0 * 2;
+  const int np = rows * static_cast<int>(ldp), nq = kStep * static_cast<int>(ldq) - col0 * 2;
+  int loaded = 0;
+  // The next step into its stage; behind the last one nothing is read, but the
+  // same number of loads is issued.
+  auto load = [&]() __attribute__((always_inline)) {
+    uint8_t* const st = smem + (loaded % kThinStages) * kThinStage;
+    const bool in = loaded < steps;
+    const auto rp = buffer(bp, in ? np : 0), rq = buffer(bq, in ? nq : 0);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rp, (__attribute__((address_space(3))) void*)(st + (wave * 2 + j) * 1024),
+                                               16, vp[j], 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rq, (__attribute__((address_space(3))) void*)(st + 8192 + (wave * 2 + j) * 1024), 16, vq[j], 0, 0, 0);
+    }
+    bp += kStep * 2;
+    bq += kStep * ldq;
+    ++loaded;
+  };
+  for (int i = 0; i < kThinStages - 1; ++i) load();
+  const int tr_row = fg * 8 + (fr >> 2);
+  const uint32_t base = runs::lds_off(smem);
+  const uint32_t op0 = base + fr * 128 + ((fg ^ (fr & 7)) << 4), op1 = base + fr * 128 + (((4 + fg) ^ (fr & 7)) << 4);
+  const uint32_t oq = base + 8192 + tr_row * 128 + ((wave ^ (tr_row & 3)) << 5) + (fr & 3) * 8;
+  f32x4 acc[4] = {};
+  for (int t = 0; t < steps; ++t) {
+    fence();
+    wait_vm<4 * (kThinStages - 2)>();  // this step's loads, of seven steps' in flight
+    barrier();                         // all wavefronts', and all have read the step before
+    load();
+    const uint32_t at = (t % kThinStages) * kThinStage;
+    bf16x8 fp[2][4];
+    s16x4 q[4];
+    // Reads and wait in one statement: the compiler would otherwise wait for the
+    // loads in flight, which go to other stages.
+    asm volatile(
+        "ds_read_b64_tr_b16 %8, %14\n\t"
+        "ds_read_b64_tr_b16 %9, %14 offset:512\n\t"
+        "ds_read_b128 %0, %12\n\t"
+        "ds_read_b128 %1, %12 offset:2048\n\t"
+        "ds_read_b128 %2, %12 offset:4096\n\t"
+        "ds_read_b128 %3, %12 offset:6144\n\t"
+        "ds_read_b64_tr_b16 %10, %14 offset:4096\n\t"
+        "ds_read_b64_tr_b16 %11, %14 offset:4608\n\t"
+        "ds_read_b128 %4, %13\n\t"
+        "ds_read_b128 %5, %13 offset:2048\n\t"
+        "ds_read_b128 %6, %13 offset:4096\n\t"
+        "ds_read_b128 %7, %13 offset:6144\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(fp[0][0]), "=&v"(fp[0][1]), "=&v"(fp[0][2]), "=&v"(fp[0][3]), "=&v"(fp[1][0]), "=&v"(fp[1][1]),
+          "=&v"(fp[1][2]), "=&v"(fp[1][3]), "=&v"(q[0]), "=&v"(q[1]), "=&v"(q[2]), "=&v"(q[3])
+        : "v"(op0 + at), "v"(op1 + at), "v"(oq + at)
+        : "memory");
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const bf16x8 fq = __builtin_bit_cast(bf16x8, __builtin_shufflevector(q[2 * k], q[2 * k + 1], 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq, fp[k][i], acc[i], 0, 0, 0);
+    }
+  }
+  fence();
+  wait_vm<0>();
+  const int line = a.K * 2;
+  const auto rd = buffer(static_cast<uint8_t*>(a.D) + row0 * line + col0 * 2, rows * line - col0 * 2);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+    const u32x2 w{pack_bf16x2(acc[i][0], acc[i][1]), pack_bf16x2(acc[i][2], acc[i][3])};
+    __builtin_amdgcn_raw_buffer_store_b64(w, rd, (i * 16 + fr) * line + wave * 32 + fg * 8, 0, 0);
+  }
+#endif
+}
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 int32_t check_sizes(int64_t M, int32_t N, int32_t K, int32_t G) {
@@ -567,6 +678,23 @@ int32_t launch(const GradArgs& a, void* stream) {
   return MOE_OK;
 }
 
+int32_t launch_thin(const GradArgs& a, void* stream) {
+  constexpr int lds = kThinStages * kThinStage;
+  static std::once_flag once[64];
+  static bool ok[64] = {};
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return MOE_EDEVICE;
+  std::call_once(once[dev], [&]() {
+    ok[dev] = hipFuncSetAttribute(reinterpret_cast<const void*>(dgrad_thin_kernel),
+                                  hipFuncAttributeMaxDynamicSharedMemorySize, lds) == hipSuccess;
+  });
+  if (!ok[dev]) return MOE_EDEVICE;
+  const int64_t grid = (a.M + 63) / 64 * (a.K / 64);
+  dgrad_thin_kernel<<<static_cast<unsigned>(grid), 256, lds, static_cast<hipStream_t>(stream)>>>(a);
+  MOE_CHECK_LAUNCH();
+  return MOE_OK;
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -582,6 +710,10 @@ extern "C" int32_t grouped_gemm_contig_dgrad(const void* dC, const void* B, void
   if (!aligned16(dC) || !aligned16(B) || !aligned16(dA)) return MOE_EUNSUPPORTED;
   const GradArgs a{static_cast<const uint8_t*>(dC), static_cast<const uint8_t*>(B), dA, m_indices, nullptr,
                    nullptr, M, N, K, G};
+  // Fewer tiles of 256 x 256 (at most one for each 128 rows) than half the CUs: the
+  // narrow kernel.  See there; at half of them the two are level.
+  const int64_t tiles = (M + 127) / 128 * ((K + 255) / 256);
+  if (2 * tiles <= grid_size()) return launch_thin(a, stream);
   return launch<false, false, false>(a, stream);
 }
 

@@ -710,10 +710,12 @@ extern "C" int32_t grouped_gemm_contig_dgrad(const void* dC, const void* B, void
   if (!aligned16(dC) || !aligned16(B) || !aligned16(dA)) return MOE_EUNSUPPORTED;
   const GradArgs a{static_cast<const uint8_t*>(dC), static_cast<const uint8_t*>(B), dA, m_indices, nullptr,
                    nullptr, M, N, K, G};
-  // Fewer tiles of 256 x 256 (at most one for each 128 rows) than half the CUs: the
-  // narrow kernel.  See there; at half of them the two are level.
+  // 256 x 256 tiles (at most one for each 128 rows and 256 columns) for fewer than
+  // two CUs in five: the narrow kernel.  Its time grows with them, the wide one's
+  // does not: N 4096, 64 tiles 50 against 74 us, 128 tiles 105 against 83; N 1024,
+  // 64 tiles 19 against 28, 128 tiles 36 against 30.
   const int64_t tiles = (M + 127) / 128 * ((K + 255) / 256);
-  if (2 * tiles <= grid_size()) return launch_thin(a, stream);
+  if (5 * tiles <= 2 * grid_size()) return launch_thin(a, stream);
   return launch<false, false, false>(a, stream);
 }
 

@@ -82,6 +82,19 @@ def test_input_gradient_of_many_runs(G, N, K):
     assert same_bits(dA[pad], before[pad])
 
 
+def test_input_gradient_rows_are_the_same_in_either_kernel():
+    """Few rows take the narrow kernel, many the wide one: a row's bits agree."""
+    announce("dgrad narrow and wide")
+    N, K = 640, 1408
+    dC, B = randn(1, 6000, N).to(DEV), randn(2, 1, N, K).to(DEV)
+    wide = torch.zeros(6000, K, dtype=BF, device=DEV)      # 47 * 6 tiles
+    L.grouped_gemm_contig_dgrad(dC, B, wide, torch.zeros(6000, dtype=torch.int32, device=DEV))
+    for n in (1, 63, 64, 65, 130, 1000):                   # at most 8 * 6
+        part = torch.zeros(n, K, dtype=BF, device=DEV)
+        L.grouped_gemm_contig_dgrad(dC[:n].contiguous(), B, part, torch.zeros(n, dtype=torch.int32, device=DEV))
+        assert same_bits(part, wide[:n]), n
+
+
 def test_a_product_longer_than_the_waits_count():
     """One expert, one tile, a long reduction, against 64 bits."""
     announce("long reduction")

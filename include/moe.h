@@ -444,7 +444,8 @@ int32_t silu_and_mul_bwd(const void* gateup, const void* dact, int64_t M, int32_
  *   grouped_gemm_contig.  Rows with m_indices < 0 are left as they were.
  *   A row's result depends on its own dC row and its expert's weights alone.
  * Limits: N % 128 == 0, K % 128 == 0, N, K <= 4194304, G <= 1024,
- * ceil(M / 128) <= 8176 -> else MOE_EUNSUPPORTED. */
+ * ceil(M / 128) <= 8160, tile positions G * ceil(N / 256) * ceil(K / 256) / 8 and
+ * ceil(M / 128) * ceil(K / 256) below 2^30 -> else MOE_EUNSUPPORTED. */
 int32_t grouped_gemm_contig_dgrad(const void* dC, const void* B, void* dA,
                                   const int32_t* m_indices, int64_t M, int32_t N, int32_t K,
                                   int32_t G, void* stream);

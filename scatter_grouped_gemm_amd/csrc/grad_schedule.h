@@ -97,10 +97,10 @@ __device__ __forceinline__ void deal(Dealer& d, Lds* L, int2* raw, const int32_t
     }
     L->range[rank] = r;
     L->id[rank] = e;
-    live += r.y > 0 || !skip_empty;
+    live += r.y > 0;
   }
-  int2 tot;
-  runs::scan_excl_sum2<WAVES>(live, 0, L->scr, tot);
+  int2 tot = make_int2(G, 0);
+  if (skip_empty) runs::scan_excl_sum2<WAVES>(live, 0, L->scr, tot);
   d.G = uniform(tot.x);
   __syncthreads();
   int r[2], c[2];

@@ -49,7 +49,8 @@ def test_product_gradients_refuse():
         c, a, s, n, dt, acc, b, M, N, K, G, None)
     for f in (d, w):
         for kw, want in [(dict(M=-1), 1), (dict(N=0), 1), (dict(K=-128), 1), (dict(G=-1), 1), (dict(N=200), 2),
-                         (dict(K=64), 2), (dict(N=8388608), 2), (dict(K=8388608), 2), (dict(M=8177 * 128), 2),
+                         (dict(K=64), 2), (dict(N=8388608), 2), (dict(K=8388608), 2), (dict(M=8160 * 128 + 1), 2),
+                         (dict(N=1 << 22, K=1 << 22, G=1024), 2),
                          (dict(G=1025), 2), (dict(c=None), 1), (dict(a=None), 1), (dict(b=None), 1),
                          (dict(a=P + 8), 2), (dict(b=P + 2), 2), (dict(c=P + 4), 2), (dict(G=0), 0)]:
             assert f(**kw) == want, (f, kw)

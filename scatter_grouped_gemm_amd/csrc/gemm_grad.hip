@@ -24,6 +24,20 @@
 //     over the phases as 8, 4, 8, 4 KB a wavefront and Q's registers need no copy.
 //   - The loop is one stream of steps over all of a workgroup's tiles: the loads
 //     cross into the next tile while the current one is finished.
+//   - Tiles: dgrad in the order of gemm_runs.h, wgrad as grad_schedule.h deals them.
+//
+// Measured (TFLOP/s; in brackets torch's library product of such sizes with the
+// same layout): 4096 rows by 8192 by 4096 dgrad 186 us, 1480 (1236-1390); 8 experts
+// of 1024 rows, N 28672, K 4096 dgrad 1.49 ms, 1290, wgrad 1.65-1.75 ms, 1100-1160;
+// one expert of 16384 rows, 4096 x 4096 wgrad 390-410 us, 1340-1400.  64 ragged
+// experts (N 2816, K 2048, 4662 rows) dgrad 141 us: B is read at 5.5 TB/s.
+// What bounds them: dgrad the card's power (matrix cores busy 81% of the cycles at
+// 1.55 GHz); wgrad the load parts (busy 57-67% at 1.8 GHz: its P takes twice the
+// LDS instructions) and, with short reductions, the stores (without them the 8
+// experts above take 12% less).  No LDS bank conflicts.  Tried without gain: the
+// reads spread evenly over the phases, 32x32x16 instructions, leaving out the
+// MFMAs of a short tile's empty rows, both groups storing at once, a staggered
+// start, non-temporal stores, other tile orders.
 #include <mutex>
 #include <type_traits>
 

@@ -44,47 +44,14 @@
 #include "common.h"
 #include "gemm_runs.h"
 #include "grad_schedule.h"
+#include "grad_tile.h"
 
 namespace moe {
 namespace {
 
-typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
-typedef __attribute__((ext_vector_type(4))) float f32x4;
-typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
-typedef __attribute__((ext_vector_type(4))) short s16x4;
-
 constexpr int kThreads = 512;
 constexpr int kTileN = 256;
-constexpr int kStep = 64;   // of the reduction
-constexpr int kGroupN = 8;  // wgrad: tiles along N of a block of the tile order
-
-struct GradArgs {
-  const uint8_t* P;   // dC [M][N]
-  const uint8_t* Q;   // dgrad: B [G][N][K]; wgrad: A [M][K]
-  void* D;            // dgrad: dA [M][K]; wgrad: dB [G][N][K]
-  const int32_t* m_indices;
-  const int32_t* starts;
-  const int32_t* counts;
-  int64_t M;
-  int N, K, G;
-};
-
-using runs::wait_vm;
 using sched::kMaxG;
-
-__device__ __forceinline__ void fence() {
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("" ::: "memory");
-}
-// A barrier that nothing crosses.
-__device__ __forceinline__ void barrier() {
-  fence();
-  __builtin_amdgcn_s_barrier();
-  fence();
-}
-__device__ __forceinline__ void wait_lds() {
-  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
-}
 
 // A tile as both sides of the stream see it.
 struct Tile {
@@ -94,41 +61,12 @@ struct Tile {
   int steps;    // of 64 of the reduction, an even number
 };
 
-// No more than `bytes` from base: reads behind them give zeros, writes are dropped.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t* base, int bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, bytes > 0 ? bytes : 0, 0x00020000);
-}
-
 // A copy that the compiler takes for a new value.  What is worked out from it
 // once in a tile would otherwise be kept in registers over the whole loop, and
 // there are more such values than registers.
 __device__ __forceinline__ int fresh_copy(int x) {
   asm volatile("" : "+s"(x));
   return x;
-}
-
-// Exchanges a of the lanes 16 .. 31 (48 .. 63) with b of the lanes 0 .. 15
-// (32 .. 47), and c with d: (a, b, c, d) afterwards.
-__device__ __forceinline__ f32x4 swap_rows(float a, float b, float c, float d) {
-  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
-  const auto q = __builtin_amdgcn_permlane16_swap(__float_as_uint(c), __float_as_uint(d), false, false);
-  return f32x4{__uint_as_float(r[0]), __uint_as_float(r[1]), __uint_as_float(q[0]), __uint_as_float(q[1])};
-}
-
-// The lanes 8 .. 15 of each 16 take b of the lanes 0 .. 7 for a, and these take
-// a of the lanes 8 .. 15 for b.  Done twice, everything is where it was.
-__device__ __forceinline__ void trade8(u32x4& a, u32x4& b) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const uint32_t x = a[e], y = b[e];
-    a[e] = __builtin_amdgcn_update_dpp(x, y, 0x128 /* row_ror:8 */, 0xf, 0xc, false);
-    b[e] = __builtin_amdgcn_update_dpp(y, x, 0x128, 0xf, 0x3, false);
-  }
-}
-
-__device__ __forceinline__ s16x4 read_tr(const uint8_t* p) {
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-      (__attribute__((address_space(3))) s16x4*)(p));
 }
 
 template <bool WGRAD, bool F32, bool ACC>
@@ -372,17 +310,7 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
     // registers that the fragments need
     int l = lane;
     asm volatile("" : "+v"(l));
-    const int row = l & 15, g = l >> 4;
-    // A store of a wavefront covers eight rows and a whole 128-byte line of
-    // each (16 rows of half a line take the texture unit longer).  A lane's
-    // accumulators are four columns of row `row` in each 16-column block, so
-    // lanes trade: bf16, first with the lane 16 on (swap_rows: eight columns in
-    // a row, of block 0 in even lane groups and of block 1 in odd ones); then the
-    // lanes 0 .. 7 of each 16 give the second half of their line for the first
-    // half of the row eight on (trade8).
-    const int col = F32 ? g * 4 + (row >> 3) * 16 : (g & 1) * 16 + (g >> 1) * 8 + (row >> 3) * 32;
     const int line = K * ES;  // 64 rows of it are at most 2^30 bytes
-    const uint32_t off = (row & 7) * line + col * ES;
 #pragma unroll
     for (int hp = 0; hp < 2; ++hp) {
       const int r0 = hp * 128 + wm * 64;  // of the tile
@@ -390,59 +318,7 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
       int rows = WGRAD ? N - ct.pt * kTileN - r0 : ct.rows - r0;
       rows = rows < 64 ? rows : 64;
       const int bytes = col0 < K && rows > 0 ? rows * line - col0 * ES : 0;
-      const auto rd = buffer(static_cast<uint8_t*>(a.D) + first * line + col0 * ES, bytes);
-      constexpr int NQ = F32 ? 2 : 1;  // lines of a row
-      u32x4 old[4][NQ][2];
-      if constexpr (ACC) {  // all of a half in flight together
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int q = 0; q < NQ; ++q)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              old[i][q][h] = __builtin_amdgcn_raw_buffer_load_b128(rd, off + (i * 16 + h * 8) * line + q * 128, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t at = off + i * 16 * line;
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          u32x4 w[2];
-          if constexpr (ACC) trade8(old[i][q][0], old[i][q][1]);
-          if constexpr (F32) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              f32x4 v = acc[hp][q][i][j];
-              if constexpr (ACC) v += __builtin_bit_cast(f32x4, old[i][q][j]);
-              w[j] = __builtin_bit_cast(u32x4, v);
-            }
-          } else {
-#pragma unroll
-            for (int hq = 0; hq < 2; ++hq) {
-              const f32x4 v0 = acc[hp][hq][i][0], v1 = acc[hp][hq][i][1];
-              if constexpr (ACC) {
-                // added in fp32, so that the sum is rounded once
-                const auto add = [&](uint32_t o, float lo, float hi) __attribute__((always_inline)) {
-                  return pack_bf16x2(lo + __uint_as_float(o << 16), hi + __uint_as_float(o & 0xffff0000u));
-                };
-                const f32x4 s0 = swap_rows(v0[0], v1[0], v0[1], v1[1]), s1 = swap_rows(v0[2], v1[2], v0[3], v1[3]);
-                const u32x4 o = old[i][0][hq];
-                w[hq] = u32x4{add(o[0], s0[0], s0[2]), add(o[1], s1[0], s1[2]), add(o[2], s0[1], s0[3]), add(o[3], s1[1], s1[3])};
-              } else {
-                const u32x4 o = __builtin_bit_cast(
-                    u32x4, swap_rows(__uint_as_float(pack_bf16x2(v0[0], v0[1])), __uint_as_float(pack_bf16x2(v1[0], v1[1])),
-                                     __uint_as_float(pack_bf16x2(v0[2], v0[3])), __uint_as_float(pack_bf16x2(v1[2], v1[3]))));
-                w[hq] = u32x4{o[0], o[2], o[1], o[3]};
-              }
-            }
-          }
-          trade8(w[0], w[1]);
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            __builtin_amdgcn_raw_buffer_store_b128(w[h], rd, at + h * 8 * line + q * 128, 0, 0);
-        }
-      }
+      store64<F32, ACC>(acc[hp], buffer(static_cast<uint8_t*>(a.D) + first * line + col0 * ES, bytes), line, l);
     }
     float zero = 0.0f;  // in a vector register: as constants, 128 scalar ones are taken for it
     asm volatile("" : "+v"(zero));
@@ -691,6 +567,32 @@ int32_t launch(const GradArgs& a, void* stream) {
   return MOE_OK;
 }
 
+// Which kernel takes a wgrad.  us, wide / 128 x 128 tiles (bf16; fp32 added):
+//   up to two small tiles a CU, always the small ones.  256 tiles of 256 rows 18 / 8;
+//     28 / 11, of 4096 rows 91 / 45; 101 / 48; 512 tiles of 16384 rows 350 / 264;
+//     325 / 227.  (896 tiles: 4096 rows 112 / 115; 117 / 118, 16384 rows 399 / 441;
+//     406 / 585.)
+//   up to six a CU, with few rows an expert.  1024 tiles: 64 rows 26 / 15; 38 / 29,
+//     1024 rows 46 / 36; 57 / 51, 4096 rows 117 / 118; 123 / 126; 1536 tiles: 512
+//     rows 42 / 33; 64 / 53.  (2048 tiles, 32 experts of 512 rows 56 / 55; 81 / 85.)
+//   added to fp32, with fewer yet, however many.  8 experts, 4096 x 4096: 64 rows
+//     276 / 211, 256 rows 277 / 241, 384 rows 279 / 284; 64 experts, 2048 x 1408: 64
+//     rows 316 / 294, 256 rows 342 / 333, 384 rows 369 / 378; 8 experts, 28672 x 4096:
+//     64 rows 1618 / 1366 (5.5 TB/s), 512 rows 1779 / 1902.  (Not so in bf16: 8
+//     experts, 4096 x 4096, 64 rows 78 / 86, added 119 / 131.)
+// Rows are M over G, which the host knows; rows dealt unevenly change little (64
+// experts, 2048 x 1408, fp32 added, 8192 rows in one and two in each other 401 / 363).
+template <bool F32, bool ACC>
+int32_t launch_wgrad(const GradArgs& a, void* stream) {
+  const int64_t tiles = static_cast<int64_t>(a.N / 128) * (a.K / 128) * a.G;
+  const int64_t cus = grid_size(), G = a.G;
+  if (cus == 0) return MOE_EDEVICE;
+  if (tiles <= 2 * cus || (tiles <= 6 * cus && a.M <= 1024 * G) ||
+      (F32 && ACC && a.M <= 256 * G && tiles < (1 << 23)))
+    return launch_wgrad_short(a, F32, ACC, static_cast<hipStream_t>(stream));
+  return launch<true, F32, ACC>(a, stream);
+}
+
 int32_t launch_thin(const GradArgs& a, void* stream) {
   constexpr int lds = kThinStages * kThinStage;
   static std::once_flag once[64];
@@ -746,6 +648,6 @@ extern "C" int32_t grouped_gemm_contig_wgrad(const void* dC, const void* A,
   const GradArgs a{static_cast<const uint8_t*>(dC), static_cast<const uint8_t*>(A), dB, nullptr,
                    expert_start_loc, num_valid, M, N, K, G};
   if (out_dtype == MOE_DTYPE_FP32)
-    return accumulate ? launch<true, true, true>(a, stream) : launch<true, true, false>(a, stream);
-  return accumulate ? launch<true, false, true>(a, stream) : launch<true, false, false>(a, stream);
+    return accumulate ? launch_wgrad<true, true>(a, stream) : launch_wgrad<true, false>(a, stream);
+  return accumulate ? launch_wgrad<false, true>(a, stream) : launch_wgrad<false, false>(a, stream);
 }

@@ -625,12 +625,23 @@ extern "C" int32_t grouped_gemm_contig_dgrad(const void* dC, const void* B, void
   if (!aligned16(dC) || !aligned16(B) || !aligned16(dA)) return MOE_EUNSUPPORTED;
   const GradArgs a{static_cast<const uint8_t*>(dC), static_cast<const uint8_t*>(B), dA, m_indices, nullptr,
                    nullptr, M, N, K, G};
-  // 256 x 256 tiles (at most one for each 128 rows and 256 columns) for fewer than
-  // two CUs in five: the narrow kernel.  Its time grows with them, the wide one's
-  // does not: N 4096, 64 tiles 50 against 74 us, 128 tiles 105 against 83; N 1024,
-  // 64 tiles 19 against 28, 128 tiles 36 against 30.
-  const int64_t tiles = (M + 127) / 128 * ((K + 255) / 256);
-  if (5 * tiles <= 2 * grid_size()) return launch_thin(a, stream);
+  // 64 x 64 tiles (thin) as long as each has a CU, 128 x 128 ones up to three for
+  // two CUs.  us, thin / 128 x 128 / 256 x 256:
+  //   256 of 64 x 64:  N 4096, 1024 rows, K 1024 26 / 38 / 74; N 14336, 512 rows,
+  //     K 2048 81 / 123 / 229
+  //   512 of 64 x 64:  N 4096, 2048 rows, K 1024 49 / 39 / 76; N 14336, 1024 rows,
+  //     K 2048 155 / 127 / 229 (but 8 experts of 17 rows, N 4096, K 2048: half of
+  //     the 64 x 64 tiles are empty, which M does not show, and thin is ahead)
+  //   256 of 128 x 128:  N 4096, 1024 rows, K 4096 96 / 43 / 77; 8 experts of 256
+  //     rows, N 14336, K 2048 320 / 179 / 261
+  //   384 of 128 x 128:  8 experts of 300 rows, K 2048, N 2816 86 / 46 / 59, N 14336
+  //     395 / 259 / 266
+  //   512 of 128 x 128:  N 4096, 2048 rows, K 4096 185 / 69 / 84; 64 experts of 73
+  //     rows, K 1024 204 / 126 / 105
+  const int64_t cus = grid_size();
+  if (cus == 0) return MOE_EDEVICE;
+  if ((M + 63) / 64 * (K / 64) <= cus) return launch_thin(a, stream);
+  if (2 * ((M + 127) / 128 * (K / 128)) <= 3 * cus) return launch_dgrad_short(a, static_cast<hipStream_t>(stream));
   return launch<false, false, false>(a, stream);
 }
 

@@ -1,4 +1,5 @@
-// What the kernels of the gradient products share (gemm_grad.hip, wgrad_short.hip):
+// What the kernels of the gradient products share (gemm_grad.hip,
+// dgrad_short.hip, wgrad_short.hip):
 // their arguments, buffer descriptors, the transposing read and the stores of a
 // wavefront's outputs.
 #pragma once
@@ -24,6 +25,10 @@ struct GradArgs {
 // wgrad_short.hip: dB of f32 or bf16, overwritten or (acc) added to.  Arguments are
 // checked by the caller; there are fewer than 2^23 tiles of 128 x 128 over all experts.
 int32_t launch_wgrad_short(const GradArgs& a, bool f32, bool acc, hipStream_t stream);
+
+// dgrad_short.hip: arguments are checked by the caller; there are fewer than 2^23
+// tiles of 128 x 128.
+int32_t launch_dgrad_short(const GradArgs& a, hipStream_t stream);
 
 namespace {
 

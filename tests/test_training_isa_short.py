@@ -74,3 +74,37 @@ def test_stores_of_a_tile(kernels):
     for key, lines in kernels[0].items():
         assert sum(line.startswith("buffer_store_dwordx4") for line in lines) == (16 if key[0] else 8), key
         assert not [x for x in lines if re.match(r"(global|flat)_store|buffer_store(?!_dwordx4)|global_atomic", x)], key
+
+
+def test_the_input_gradient_of_few_tiles(tmp_path):
+    """The same for its 128 x 128 tiles: eight loads a step, no wait between a step's
+    barriers, eight stores, nothing spilled."""
+    if not os.path.exists(HIPCC):
+        pytest.skip("hipcc not available")
+    from scatter_grouped_gemm_amd import build
+    out = tmp_path / "dgrad_short.s"
+    subprocess.run([HIPCC, *build.FLAGS, "--cuda-device-only", "-S", os.path.join(CSRC, "dgrad_short.hip"), "-o", str(out)],
+                   check=True, capture_output=True)
+    text = out.read_text()
+    assert not re.search(r"\bscratch_(load|store)", text)
+    lines = [x.split(";")[0].strip() for x in text[:text.index(".Lfunc_end")].splitlines()]
+    at = [i for i, line in enumerate(lines) if line.startswith("s_barrier")]
+    assert len(at) == 4
+    first, read, second, again = at
+    parts = [lines[:first], lines[first:read], lines[read:second], lines[second:again], lines[again:]]
+    assert [sum(map(_is_load, p)) for p in parts] == [16, 0, 8, 0, 8]
+    assert [sum(x.startswith("v_mfma") for x in p) for p in parts] == [0, 32, 0, 32, 0]
+    assert [sum(x.startswith("ds_read") for x in p) for p in parts] == [0, 24, 0, 24, 0]
+    start = next(i for i, x in enumerate(parts[0]) if _is_load(x))
+    for p in (parts[0][start:], parts[2]):
+        waits = [x for x in p if "vmcnt" in x]
+        assert len(waits) == 1 and re.match(r"s_waitcnt vmcnt\(8\)", waits[0]), waits
+        assert not any(_is_load(x) for x in p[p.index(waits[0]):])
+    for p in (parts[1], parts[3]):
+        assert not any("vmcnt" in x for x in p)
+        last = max(i for i, x in enumerate(p) if x.startswith("ds_read"))
+        assert any("lgkmcnt(0)" in x for x in p[last:])
+    ended = [x for x in parts[4] if x.startswith("s_waitcnt vmcnt")]
+    assert re.match(r"s_waitcnt vmcnt\(0\)", ended[0])
+    assert sum(line.startswith("buffer_store_dwordx4") for line in lines) == 8
+    assert not [x for x in lines if re.match(r"(global|flat)_store|buffer_store(?!_dwordx4)|global_atomic", x)]

@@ -161,10 +161,10 @@ __global__ __launch_bounds__(256, 8) void adamw_kernel(const uint8_t* __restrict
                                                     const float* __restrict__ grad_scale,
                                                     int64_t* counter, double beta1, double beta2,
                                                     float eps, uint32_t seed) {
-  // The reciprocal of each scale, taken as powf(2, -e), which is the product that
-  // torch.ldexp makes on this card: within 2^-24 of 2^-e.  What is cut at random
-  // does not mind its last place, and a program in torch gets the same codes, bit
-  // for bit.
+  // The reciprocal of each scale, taken as powf(2, -e): within 2^-24 of 2^-e, and
+  // what a torch program that scales by a power multiplies by on this card.  What
+  // is cut at random does not mind its last place, and such a program gets the same
+  // codes, bit for bit.
   __shared__ float inverse[256];
   float two = 2.0f;
   asm volatile("" : "+v"(two));  // as a constant it becomes exp2f, which is another function

@@ -26,11 +26,15 @@
 //     cross into the next tile while the current one is finished.
 //   - Tiles: dgrad in the order of gemm_runs.h, wgrad as grad_schedule.h deals them.
 //
-// Measured (TFLOP/s; in brackets torch's library product of such sizes with the
-// same layout): 4096 rows by 8192 by 4096 dgrad 186 us, 1480 (1236-1390); 8 experts
-// of 1024 rows, N 28672, K 4096 dgrad 1.49 ms, 1290, wgrad 1.65-1.75 ms, 1100-1160;
-// one expert of 16384 rows, 4096 x 4096 wgrad 390-410 us, 1340-1400.  64 ragged
-// experts (N 2816, K 2048, 4662 rows) dgrad 141 us: B is read at 5.5 TB/s.
+// Where 256 x 256 tiles do not fill the card, or hold a few steps only, smaller
+// ones take the call: dgrad_thin_kernel below, dgrad_short.hip, wgrad_short.hip.
+//
+// Measured (TFLOP/s; in brackets torch's library product of one matrix with the same
+// layout): 4096 rows by 8192 by 4096 dgrad 186 us, 1480 (8192 rows: 1236-1390); 8
+// experts of 1024 rows, N 28672, K 4096 dgrad 1.34-1.49 ms, 1290-1440, wgrad
+// 1.65-1.75 ms, 1100-1160 (one of the experts alone 1004); one expert of 16384 rows,
+// 4096 x 4096 wgrad 390-410 us, 1340-1400 (997).  64 ragged experts (N 2816, K 2048,
+// 4662 rows) dgrad 141 us: B is read at 5.5 TB/s.
 // What bounds them: dgrad the card's power (matrix cores busy 81% of the cycles at
 // 1.55 GHz); wgrad the load parts (busy 57-67% at 1.8 GHz: its P takes twice the
 // LDS instructions) and, with short reductions, the stores (without them the 8

@@ -400,7 +400,8 @@ int32_t moe_combine(const void* Y, int64_t num_rows, const int32_t* src2dst,
  *   Rows of dY that no slot names (padding) are left as they were.  The rows
  *   named must be distinct (as the scatter leaves them); a row named twice gets
  *   one of its two values.  dY must not overlap the inputs.
- * Limits: H % 8 == 0, 1 <= k <= 32. */
+ * Limits: H % 8 == 0, H <= 2^30, 1 <= k <= 32, T times the lesser of H / 8 (rounded
+ * up to 64) and 1024 below 2^32. */
 int32_t moe_combine_bwd(const void* dout, const void* Y, int64_t num_rows, const int32_t* src2dst,
                         const float* topk_weights, int32_t T, int32_t k, int32_t H, void* dY,
                         float* dtopk_weights, void* stream);
@@ -411,7 +412,7 @@ int32_t moe_combine_bwd(const void* dout, const void* Y, int64_t num_rows, const
  * (all fp32; an id named twice gets the sum of its terms, ids outside [0, E)
  * are skipped).  Linear in dw: where the experts are shared out, the shares'
  * results add up to the whole gradient.
- *   dlogits fp32 [T][E].  Limits as moe_route_topk. */
+ *   dlogits fp32 [T][E].  Limits as moe_route_topk, T < 2^26. */
 int32_t moe_route_topk_bwd(const int32_t* topk_ids, const float* topk_weights,
                            const float* dtopk_weights, int32_t T, int32_t E, int32_t k,
                            float* dlogits, void* stream);
@@ -420,7 +421,7 @@ int32_t moe_route_topk_bwd(const int32_t* topk_ids, const float* topk_weights,
  * [0, num_rows) of dX[src2dst[t][j]][h], added in fp32 in slot order and
  * rounded once to bf16; 0 for a token without such a slot.  Serves both layouts.
  *   dX bf16 [num_rows][H]; dx bf16 [T][H].
- * Limits: H % 8 == 0, 1 <= k <= 32. */
+ * Limits as moe_combine_bwd. */
 int32_t moe_scatter_bwd(const void* dX, int64_t num_rows, const int32_t* src2dst, int32_t T,
                         int32_t k, int32_t H, void* dx, void* stream);
 
@@ -432,7 +433,7 @@ int32_t moe_scatter_bwd(const void* dX, int64_t num_rows, const int32_t* src2dst
  * each rounded once to bf16.  Rows are chosen as in silu_and_mul; skipped rows
  * are left as they were.
  *   gateup, dgateup bf16 [M][2I] (may be one buffer); dact, act bf16 [M][I].
- * Limits: I % 128 == 0, I <= 67107840. */
+ * Limits: I % 128 == 0, I <= 67107840, M < 2^26 - 3. */
 int32_t silu_and_mul_bwd(const void* gateup, const void* dact, int64_t M, int32_t I,
                          const int32_t* m_indices, const int32_t* masked_m, int32_t max_m,
                          void* dgateup, void* act, void* stream);

@@ -96,13 +96,14 @@ extern "C" int32_t moe_combine(const void* Y, int64_t num_rows, const int32_t* s
 extern "C" int32_t moe_scatter_bwd(const void* dX, int64_t num_rows, const int32_t* src2dst, int32_t T,
                                    int32_t k, int32_t H, void* dx, void* stream) {
   if (T < 0 || k < 1 || k > 32 || H <= 0 || num_rows < 0) return MOE_EINVAL;
-  if (H % 8 != 0) return MOE_EUNSUPPORTED;
+  if (H % 8 != 0 || H > (1 << 30)) return MOE_EUNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!src2dst || !dx || (num_rows > 0 && !dX)) return MOE_EINVAL;
   if ((reinterpret_cast<uintptr_t>(dX) | reinterpret_cast<uintptr_t>(dx)) & 15) return MOE_EUNSUPPORTED;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int need = (H / 8 + 63) / 64 * 64;
   const int nt = need < 1024 ? need : 1024;
+  if (static_cast<int64_t>(T) * nt >= (1ll << 32)) return MOE_EUNSUPPORTED;  // threads of a launch
   const uint16_t* y = static_cast<const uint16_t*>(dX);
   uint16_t* o = static_cast<uint16_t*>(dx);
   if (k <= 2)

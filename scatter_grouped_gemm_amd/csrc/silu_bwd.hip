@@ -94,7 +94,7 @@ extern "C" int32_t silu_and_mul_bwd(const void* gateup, const void* dact, int64_
   if (!aligned16(gateup) || !aligned16(dact) || !aligned16(dgateup) || !aligned16(act))
     return MOE_EUNSUPPORTED;
   const int64_t nb = (M + 3) / 4, cols = (static_cast<int64_t>(I) + kPass * 512 - 1) / (kPass * 512);
-  if (nb >= (1ll << 31) || cols > 65535) return MOE_EUNSUPPORTED;
+  if (nb >= (1 << 24) || cols > 65535) return MOE_EUNSUPPORTED;  // threads of a launch, its grid
   silu_bwd_kernel<<<dim3(static_cast<unsigned>(nb), static_cast<unsigned>(cols)), 256, 0,
                     static_cast<hipStream_t>(stream)>>>(
       static_cast<const uint16_t*>(gateup), static_cast<const uint16_t*>(dact), M, I, m_indices,

@@ -150,7 +150,7 @@ extern "C" int32_t moe_combine_bwd(const void* dout, const void* Y, int64_t num_
                                    int32_t k, int32_t H, void* dY, float* dtopk_weights,
                                    void* stream) {
   if (T < 0 || k < 1 || k > 32 || H <= 0 || num_rows < 0) return MOE_EINVAL;
-  if (H % 8 != 0) return MOE_EUNSUPPORTED;
+  if (H % 8 != 0 || H > (1 << 30)) return MOE_EUNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!dout || !src2dst || !topk_weights || !dtopk_weights) return MOE_EINVAL;
   if (num_rows > 0 && (!Y || !dY)) return MOE_EINVAL;
@@ -158,6 +158,7 @@ extern "C" int32_t moe_combine_bwd(const void* dout, const void* Y, int64_t num_
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int need = (H / 8 + 63) / 64 * 64;
   const int nt = need < 1024 ? need : 1024;
+  if (static_cast<int64_t>(T) * nt >= (1ll << 32)) return MOE_EUNSUPPORTED;  // threads of a launch
   const uint16_t *g = static_cast<const uint16_t*>(dout), *y = static_cast<const uint16_t*>(Y);
   uint16_t* d = static_cast<uint16_t*>(dY);
   if (k <= 2)
@@ -174,6 +175,7 @@ extern "C" int32_t moe_route_topk_bwd(const int32_t* topk_ids, const float* topk
                                       const float* dtopk_weights, int32_t T, int32_t E, int32_t k,
                                       float* dlogits, void* stream) {
   if (T < 0 || E < 1 || E > 1024 || k < 1 || k > E || k > 32) return MOE_EINVAL;
+  if (T >= (1 << 26)) return MOE_EUNSUPPORTED;  // threads of a launch
   if (T == 0) return MOE_OK;
   if (!topk_ids || !topk_weights || !dtopk_weights || !dlogits) return MOE_EINVAL;
   hipStream_t s = static_cast<hipStream_t>(stream);

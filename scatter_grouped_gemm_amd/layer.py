@@ -248,9 +248,14 @@ class MoELayer:
     # -- training ---------------------------------------------------------------------
 
     def allocate_grads(self):
-        """The weight gradients dw13 [El, 2I, H] and dw2 [El, H, I], zero."""
+        """The weight gradients dw13 [El, 2I, H] and dw2 [El, H, I], zero (in
+        place where the layer has them).  A captured backward needs them allocated before."""
         if not self.train:
             raise ValueError("the layer was made without train=True")
+        if self.dw13 is not None:        # an optimizer may hold them
+            self.dw13.zero_()
+            self.dw2.zero_()
+            return
         self.dw13 = torch.zeros(self.El, 2 * self.I, self.H, dtype=self.grad_dtype, device=self.device)
         self.dw2 = torch.zeros(self.El, self.H, self.I, dtype=self.grad_dtype, device=self.device)
 
@@ -271,6 +276,9 @@ class MoELayer:
         if dout.shape != (T, self.H):
             raise ValueError(f"dout: want {(T, self.H)}, got {tuple(dout.shape)}")
         if self.dw13 is None:
+            # zeroed in the graph, they would be so again in every replay
+            if self.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+                raise ValueError("call allocate_grads() before backward is captured")
             self.allocate_grads()
         s2d, dx, dtw = self.src2dst[:T], self.dx[:T], self.dtopk_weights[:T]
         m_idx, starts, counts = self.m_indices, self.expert_start_loc, self.num_valid

@@ -19,7 +19,8 @@ class AdamW:
     """AdamW with decoupled weight decay.
 
     params, grads    lists of contiguous tensors of equal sizes on one device,
-                     16-byte aligned; params bf16 or fp32, grads bf16 or fp32.  A
+                     16-byte aligned; params bf16 or fp32, none overlapping
+                     another, grads bf16 or fp32.  A
                      bf16 parameter is the rounding of an fp32 master that this
                      class holds; both stay where they are between steps (write
                      new gradients into the same buffers).
@@ -62,6 +63,11 @@ class AdamW:
                 raise ValueError(f"tensor {i}: must be contiguous")
             if p.data_ptr() % 16 or g.data_ptr() % 16:
                 raise ValueError(f"tensor {i}: must be 16-byte aligned")
+        held = sorted((p.data_ptr(), p.data_ptr() + p.numel() * p.element_size(), i)
+                      for i, p in enumerate(params) if p.numel())
+        for (_, end, i), (start, _, j) in zip(held, held[1:]):
+            if start < end:          # two updates of one element would race
+                raise ValueError(f"parameters {i} and {j} share memory")
         self.params, self.grads = params, grads
         self.betas, self.eps, self.seed, self.state_bits = (float(betas[0]), float(betas[1])), float(eps), int(seed), state_bits
         self.offsets, total = [], 0
@@ -91,6 +97,7 @@ class AdamW:
                 state_bits=state_bits))
         self._plan = L.moe_adamw_plan(tensors).to(dev)
 
+    @torch.no_grad()
     def reset_master(self):
         """Take the masters of bf16 parameters from the parameters (after loading new ones)."""
         for p, at in zip(self.params, self.offsets):
@@ -103,11 +110,12 @@ class AdamW:
         return {"steps": self.steps, "offsets": list(self.offsets), "state_bits": self.state_bits,
                 **{n: getattr(self, n) for n in names if getattr(self, n) is not None}}
 
+    @torch.no_grad()
     def load_state_dict(self, state: dict):
         """Take over another run's state_dict (same tensors, same state_bits); bf16
         parameters become their masters' roundings."""
         mine = self.state_dict()
-        if state["state_bits"] != self.state_bits or list(state["offsets"]) != self.offsets or state.keys() != mine.keys():
+        if state.keys() != mine.keys() or state["state_bits"] != self.state_bits or list(state["offsets"]) != self.offsets:
             raise ValueError("the state is of other tensors or another state_bits")
         for n, t in mine.items():
             if isinstance(t, torch.Tensor):

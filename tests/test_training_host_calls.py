@@ -1,0 +1,63 @@
+"""Calls of the training operators that their documentation allows or that have to
+be refused: parameters that require gradients, tensors named twice, sizes past what
+a launch can hold (no GPU needed)."""
+import ctypes
+
+import pytest
+import torch
+
+from scatter_grouped_gemm_amd import AdamW, MoELayer
+from scatter_grouped_gemm_amd import _lib as L
+
+P = 4096  # non-null, 16-byte aligned, never dereferenced
+
+
+def test_adamw_takes_parameters_that_require_gradients():
+    p = torch.nn.Parameter(torch.randn(130).bfloat16())
+    o = AdamW([p], [torch.zeros(130).bfloat16()], state_bits=8)
+    assert not o.master.requires_grad and o.master.grad_fn is None
+    assert torch.equal(o.master[:130], p.detach().float())
+    o.reset_master()
+    saved = {k: v.clone() if isinstance(v, torch.Tensor) else v for k, v in o.state_dict().items()}
+    saved["master"] += 1
+    o.load_state_dict(saved)
+    assert torch.equal(p.detach(), saved["master"][:130].bfloat16()) and p.is_leaf and p.requires_grad
+
+
+def test_adamw_refuses_parameters_that_share_memory():
+    a, g = torch.zeros(256), torch.zeros(256)
+    for params in ([a, a], [a, a[:64]], [a[128:], a[:132]]):
+        with pytest.raises(ValueError, match="share"):
+            AdamW(params, [torch.zeros_like(p) for p in params])
+    AdamW([a[:128], a[128:]], [g[:128], g[:128]])            # neighbours; gradients may be shared
+    AdamW([a[:0], a[:0], a], [g[:0], g[:0], g])              # nothing to share
+
+
+def test_adamw_state_of_another_kind_is_a_value_error():
+    o = AdamW([torch.zeros(130)], [torch.zeros(130)])
+    with pytest.raises(ValueError):
+        o.load_state_dict({})
+    with pytest.raises(ValueError):
+        o.load_state_dict({k: v for k, v in o.state_dict().items() if k != "offsets"})
+
+
+def test_sizes_past_a_launch_are_refused():
+    lib = L.lib()
+    c = lambda T=4, k=2, H=256: lib.moe_combine_bwd(P, P, 10, P, P, T, k, H, P, P, None)  # noqa: E731
+    s = lambda T=4, k=2, H=256: lib.moe_scatter_bwd(P, 10, P, T, k, H, P, None)  # noqa: E731
+    for f in (c, s):
+        for kw in (dict(H=(1 << 30) + 8), dict(H=2147483640), dict(T=1 << 26, H=512), dict(T=1 << 22, H=8192)):
+            assert f(**kw) == L.MOE_EUNSUPPORTED, (f, kw)
+    assert lib.moe_route_topk_bwd(P, P, P, 1 << 26, 8, 2, P, None) == L.MOE_EUNSUPPORTED
+    assert lib.silu_and_mul_bwd(P, P, 1 << 26, 128, None, None, 0, P, P, None) == L.MOE_EUNSUPPORTED
+
+
+def test_gradients_are_allocated_once():
+    """An optimizer that holds them would go on reading the old ones."""
+    layer = MoELayer(num_experts=4, top_k=2, hidden=128, intermediate=128, max_tokens=8, train=True, device="cpu")
+    layer.allocate_grads()
+    a, b = layer.dw13, layer.dw2
+    a.fill_(1)
+    b.fill_(1)
+    layer.allocate_grads()
+    assert layer.dw13 is a and layer.dw2 is b and not a.any() and not b.any()

@@ -157,7 +157,8 @@ __device__ __forceinline__ void store8(void* p, bool half, int64_t i, int n, con
 // 64 registers, so that eight workgroups fit a CU: in 8 bits the arithmetic of an
 // element (two hashes, two roundings, a root) takes about as long as its 16 bytes
 // (268M elements: 934 us, 4.6 TB/s; 980 with 84 registers).
-__global__ __launch_bounds__(256, 8) void adamw_kernel(const uint8_t* __restrict__ plan, const float* __restrict__ lr,
+__global__ __launch_bounds__(256, 8) void adamw_kernel(const uint8_t* __restrict__ plan, size_t plan_bytes,
+                                                    const float* __restrict__ lr,
                                                     const float* __restrict__ grad_scale,
                                                     int64_t* counter, double beta1, double beta2,
                                                     float eps, uint32_t seed) {
@@ -173,7 +174,10 @@ __global__ __launch_bounds__(256, 8) void adamw_kernel(const uint8_t* __restrict
   const Header* const h = reinterpret_cast<const Header*>(plan);
   const moe_adamw_tensor* const tensors = reinterpret_cast<const moe_adamw_tensor*>(plan + sizeof(Header));
   const int2* const chunks = reinterpret_cast<const int2*>(tensors + h->tensors);
-  const int nchunk = h->magic == kMagic ? h->chunks : 0;
+  // a plan cut short lists nothing
+  const bool whole = h->magic == kMagic && sizeof(Header) + h->tensors * sizeof(moe_adamw_tensor) +
+                                                   h->chunks * sizeof(int2) <= plan_bytes;
+  const int nchunk = whole ? h->chunks : 0;
   const int64_t step = counter[0] + 1;
   const float rate0 = lr[0];
   const float gscale = grad_scale ? grad_scale[0] : 1.0f;
@@ -335,7 +339,7 @@ extern "C" int32_t moe_adamw_step(const void* plan, size_t plan_bytes, const flo
   const size_t most = (plan_bytes - sizeof(Header)) / sizeof(int2);
   const unsigned grid = most < 1 ? 1u : most < 2048 ? static_cast<unsigned>(most) : 2048u;
   adamw_kernel<<<grid, 256, 0, static_cast<hipStream_t>(stream)>>>(
-      static_cast<const uint8_t*>(plan), lr, grad_scale, counter, beta1, beta2, eps, seed);
+      static_cast<const uint8_t*>(plan), plan_bytes, lr, grad_scale, counter, beta1, beta2, eps, seed);
   MOE_CHECK_LAUNCH();
   return MOE_OK;
 }

@@ -1,0 +1,79 @@
+"""Calls that the training operators' documentation allows and their single tests
+do not make."""
+import pytest
+import torch
+
+from scatter_grouped_gemm_amd import AdamW
+from scatter_grouped_gemm_amd import _lib as L
+from gpu_util import DEV, announce
+from test_gpu_training import BF, F32, _make, gen, randn, same_bits
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_plan_cut_short_updates_nothing(bits):
+    announce("adamw plan cut", bits)
+    p = randn(1, 5000, dtype=F32).to(DEV)
+    before = p.clone()
+    o = AdamW([p], [torch.ones_like(p)], state_bits=bits)
+    for cut in (8, 16, 80):
+        L.moe_adamw_step(o._plan[:-cut].contiguous(), o.lr, o._counter, 0.9, 0.95, 1e-8)
+    torch.cuda.synchronize()
+    assert same_bits(p, before) and not o.m.any() and not o.v.any()
+    o.step()
+    assert not same_bits(p, before)
+
+
+def test_adamw_with_parameters_that_require_gradients():
+    announce("adamw parameters")
+    a = randn(1, 700).to(DEV)
+    b = torch.nn.Parameter(a.clone())
+    g = randn(2, 700).to(DEV)
+    x, y = AdamW([a], [g], state_bits=8), AdamW([b], [g], state_bits=8)
+    for o in (x, y, x, y):
+        o.step()
+    assert same_bits(a, b.detach()) and same_bits(x.m, y.m) and not y.master.requires_grad
+
+
+def test_a_captured_backward_needs_its_gradients():
+    announce("captured backward")
+    layer, x, logits, _, _ = _make(32, 256, 128, 8, 2)
+    xd, ld, dout = x.to(DEV), logits.to(DEV), randn(5, 32, 256).to(DEV)
+    layer(xd, ld)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        torch.zeros(8, device=DEV)
+        with pytest.raises(ValueError, match="allocate_grads"):
+            layer.backward(dout)
+    assert layer.dw13 is None
+    layer.backward(dout)                                     # the forward is still there
+
+
+def test_accumulating_over_replays_and_small_batches():
+    """Forward and an accumulating fp32 backward captured once, replayed over
+    batches: the sum of the batches' gradients, the same as eager calls."""
+    announce("accumulate replays")
+    T = 40
+    batches = [(randn(40 + i, T, 256).to(DEV), torch.randn(T, 8, generator=gen(60 + i)).to(DEV)) for i in range(3)]
+    dout = randn(5, T, 256).to(DEV)
+    eager = _make(T, 256, 128, 8, 2, grad_dtype=F32)[0]
+    for x, lg in batches:
+        eager(x, lg)
+        eager.backward(dout, accumulate=True)
+    layer = _make(T, 256, 128, 8, 2, grad_dtype=F32)[0]
+    layer.allocate_grads()
+    sx, sl = batches[0][0].clone(), batches[0][1].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer(sx, sl)
+        layer.backward(dout, accumulate=True)
+    layer.allocate_grads()
+    for x, lg in batches:
+        sx.copy_(x)
+        sl.copy_(lg)
+        graph.replay()
+        torch.cuda.synchronize()
+    assert layer.dw13.any() and same_bits(layer.dw13, eager.dw13) and same_bits(layer.dw2, eager.dw2)

@@ -101,9 +101,14 @@ extern "C" int32_t moe_scatter_bwd(const void* dX, int64_t num_rows, const int32
   if (!src2dst || !dx || (num_rows > 0 && !dX)) return MOE_EINVAL;
   if ((reinterpret_cast<uintptr_t>(dX) | reinterpret_cast<uintptr_t>(dx)) & 15) return MOE_EUNSUPPORTED;
   hipStream_t s = static_cast<hipStream_t>(stream);
+  // Rows of more than 512 threads in two passes of half as many: four workgroups on
+  // a CU in place of two, so a CU has more loads in flight (1021 tokens, H 7168, an
+  // eighth of their 8 slots held: 7.2 us, 10.0 in one pass; in four 8.7; all held
+  // 23.4, 24.4; 8192 tokens 186, 186).
   const int need = (H / 8 + 63) / 64 * 64;
-  const int nt = need < 1024 ? need : 1024;
-  if (static_cast<int64_t>(T) * nt >= (1ll << 32)) return MOE_EUNSUPPORTED;  // threads of a launch
+  const int half = (need / 2 + 63) / 64 * 64;
+  const int nt = need <= 512 ? need : half < 1024 ? half : 1024;
+  if (static_cast<int64_t>(T) * (need < 1024 ? need : 1024) >= (1ll << 32)) return MOE_EUNSUPPORTED;  // threads of a launch
   const uint16_t* y = static_cast<const uint16_t*>(dX);
   uint16_t* o = static_cast<uint16_t*>(dx);
   if (k <= 2)

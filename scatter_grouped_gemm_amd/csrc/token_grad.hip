@@ -4,7 +4,7 @@
 //   dY[r(t,j)] = w[t][j] dout[t],   dw[t][j] = <dout[t], Y[r(t,j)]>.
 // One pass reads dout once and every expert-output row once and writes every
 // gradient row once, so the kernel is bound by memory: 2 T H + 4 A H bytes for
-// A held assignments (8192 tokens, H 7168, top-8 with the routing gradient: 397
+// A held assignments (8192 tokens, H 7168, top-8 with the routing gradient: 400
 // us, 5.0 TB/s, what a plain copy reaches).
 #include "common.h"
 
@@ -36,7 +36,7 @@ __device__ __forceinline__ float reduce8(float (&v)[8], int lane, int& slot) {
 }
 
 // One workgroup per token, each thread 8 consecutive channels at a time, the
-// workgroup as wide as the row where that is at most 1024 threads.  Slots go
+// workgroup as wide as the row or half of it.  Slots go
 // in groups of eight: a group's Y rows are loaded together (independent
 // 16-byte loads in flight), multiplied into eight dot products held in fp32,
 // and the gradient rows written.  The partial sums of a token are added in an
@@ -156,9 +156,14 @@ extern "C" int32_t moe_combine_bwd(const void* dout, const void* Y, int64_t num_
   if (num_rows > 0 && (!Y || !dY)) return MOE_EINVAL;
   if (!aligned16(dout) || !aligned16(Y) || !aligned16(dY)) return MOE_EUNSUPPORTED;
   hipStream_t s = static_cast<hipStream_t>(stream);
+  // Rows of more than 512 threads in two passes of half as many: more workgroups on
+  // a CU, so more loads in flight where most slots are held elsewhere (1021 tokens,
+  // H 7168, an eighth of their 8 slots held: 11.6 us, 16.0 in one pass; all held
+  // 47.4, 48.6; 256 tokens 6.0, 5.6; 8192 tokens 377.7, 376.0).
   const int need = (H / 8 + 63) / 64 * 64;
-  const int nt = need < 1024 ? need : 1024;
-  if (static_cast<int64_t>(T) * nt >= (1ll << 32)) return MOE_EUNSUPPORTED;  // threads of a launch
+  const int half = (need / 2 + 63) / 64 * 64;
+  const int nt = need <= 512 ? need : half < 1024 ? half : 1024;
+  if (static_cast<int64_t>(T) * (need < 1024 ? need : 1024) >= (1ll << 32)) return MOE_EUNSUPPORTED;  // threads of a launch
   const uint16_t *g = static_cast<const uint16_t*>(dout), *y = static_cast<const uint16_t*>(Y);
   uint16_t* d = static_cast<uint16_t*>(dY);
   if (k <= 2)

@@ -32,8 +32,8 @@ class AdamW:
     written between steps.  ``master``, ``m``, ``v`` (and ``m_scale``,
     ``v_scale``) are flat over all tensors, tensor i at ``offsets[i]``, a
     multiple of 128; ``v`` holds the codes of its root where state_bits is 8.
-    ``state_dict`` gives
-    what a checkpoint has to keep (and the fp32 parameters, which are the caller's).
+    ``state_dict`` gives what a checkpoint has to keep (and the fp32 parameters,
+    which are the caller's).
     """
 
     def __init__(self, params, grads, *, lr: float = 1e-3, betas=(0.9, 0.95), eps: float = 1e-8,

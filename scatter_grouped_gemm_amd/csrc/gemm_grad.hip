@@ -101,8 +101,8 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
   } else {
     runs::Share sh;
     static_assert(runs::kMaxBlocks * 4 <= 32768, "the set-up arrays fit in the stages");
-    if (!runs::build_share<8>(a.m_indices, a.M, a.G, ntk, reinterpret_cast<int*>(q0),
-                              reinterpret_cast<int*>(q1), reinterpret_cast<int*>(p00), table, sh))
+    if (!runs::build_share<8, true>(a.m_indices, a.M, a.G, ntk, reinterpret_cast<int*>(q0),
+                                    reinterpret_cast<int*>(q1), reinterpret_cast<int*>(p00), table, sh))
       return;
     NR = sched::uniform(sh.NR);
     pos = sched::uniform(sh.lo) + static_cast<int>(blockIdx.x >> 3);

@@ -3,8 +3,9 @@
 // position -> tile decoder, and the small LDS and wait helpers the kernel uses
 // around it.
 //
-// Order: expert runs (maximal stretches of 128-row blocks with one expert id)
-// in row order; a run of z valid rows is cut into ceil(z / 256) M-tiles of
+// Order: expert runs (maximal stretches of 128-row blocks with one expert id;
+// for the gradient, which may not write padding rows, a block that is not full
+// ends its run) in row order; a run of z valid rows is cut into ceil(z / 256) M-tiles of
 // equal height (rounded up to the kernel's row quantum); inside a run, groups
 // of up to kGM M-tiles, N-tiles in order, the group's M-tiles innermost, so
 // the workgroups of an XCD running side by side share weight panels (few
@@ -153,24 +154,43 @@ struct Share {
 // ints each) and 2 * WAVES ints for the scans.  All 64 * WAVES threads call it;
 // it ends with a barrier.  Returns false when the workgroup has no position to
 // run.
-template <int WAVES>
+// FULL: the rows of a run are all valid (a block whose last row is not ends it);
+// otherwise only its last block's are counted, and the padding of an earlier one
+// is taken for rows of the run.  It reads that row of every block too: 6400 blocks,
+// N and K 256 218 us, 209 without; up to 600 blocks no difference.
+// Every run has a tile, and a share no more tiles than an eighth of the blocks
+// and two, so kTable entries hold the runs of either kind.
+constexpr int kPartial = 1 << 16;  // in ids: the block is not full (ids are below 1024 then)
+static_assert(kMaxBlocks / 8 + 2 <= kTable, "the run table holds a share of single blocks");
+template <int WAVES, bool FULL = false>
 __device__ __forceinline__ bool build_share(const int32_t* __restrict__ m_indices, int64_t M, int G,
                                             int ntn, int* ids, int* zv, int* scr, int4* table, Share& sh) {
   constexpr int kThreads = 64 * WAVES;
   const int tid = threadIdx.x;
   const int nblk = static_cast<int>((M + 127) / 128);
-  for (int j = tid; j < nblk; j += kThreads) {
-    const int v = m_indices[static_cast<int64_t>(j) * 128];
-    ids[j] = (v >= 0 && v < G) ? v : -1;
+  if constexpr (FULL) {
+#pragma unroll 4
+    for (int j = tid; j < nblk; j += kThreads) {
+      const int32_t* const b = m_indices + static_cast<int64_t>(j) * 128;
+      const int v = b[0], end = b[j + 1 < nblk ? 127 : 0];  // both loads in flight together
+      ids[j] = (v < 0 || v >= G) ? -1 : end < 0 ? v | kPartial : v;
+    }
+  } else {
+    for (int j = tid; j < nblk; j += kThreads) {
+      const int v = m_indices[static_cast<int64_t>(j) * 128];
+      ids[j] = (v >= 0 && v < G) ? v : -1;
+    }
   }
   __syncthreads();
+  // expert of block j, negative: none
+  const auto id = [&](int j) { return FULL && ids[j] >= 0 ? ids[j] & (kPartial - 1) : ids[j]; };
   const int PB = (nblk + kThreads - 1) / kThreads;
   const int j0 = min(tid * PB, nblk), j1 = min(j0 + PB, nblk);
   // block j starts a run if its id differs from the block before; ends one if
-  // the block after differs
+  // the block after differs (from a marked block every id does)
   int ls = -1;
   for (int j = j0; j < j1; ++j)
-    if (ids[j] >= 0 && (j == 0 || ids[j - 1] != ids[j])) ls = j;
+    if (ids[j] >= 0 && (j == 0 || ids[j - 1] != id(j))) ls = j;
   const int carry = max(scan_excl_max<WAVES>(ls, scr), -1);
   // runs ending in this thread's blocks: their valid rows (the last block's
   // valid rows come first, so a binary search for its first negative entry)
@@ -179,9 +199,9 @@ __device__ __forceinline__ bool build_share(const int32_t* __restrict__ m_indice
   {
     int S = carry;
     for (int j = j0; j < j1; ++j) {
-      const int v = ids[j];
+      const int v = id(j);
       if (v >= 0 && (j == 0 || ids[j - 1] != v)) S = j;
-      if (v >= 0 && (j == nblk - 1 || ids[j + 1] != v)) {
+      if (v >= 0 && (j == nblk - 1 || id(j + 1) != ids[j])) {
         const int64_t r0 = static_cast<int64_t>(j) * 128;
         int lo = 1, hi = M - r0 < 128 ? static_cast<int>(M - r0) : 128;
         while (lo < hi) {
@@ -208,9 +228,9 @@ __device__ __forceinline__ bool build_share(const int32_t* __restrict__ m_indice
   {
     int S = carry, mb = base.y;
     for (int j = j0; j < j1; ++j) {
-      const int v = ids[j];
+      const int v = id(j);
       if (v >= 0 && (j == 0 || ids[j - 1] != v)) S = j;
-      if (v >= 0 && (j == nblk - 1 || ids[j + 1] != v)) {
+      if (v >= 0 && (j == nblk - 1 || id(j + 1) != ids[j])) {
         const int nt = tiles_of(zv[j]);
         if ((mb + nt) * ntn <= lo_x) ++c_lo;
         if (mb * ntn < hi_x) ++c_hi;
@@ -224,9 +244,9 @@ __device__ __forceinline__ bool build_share(const int32_t* __restrict__ m_indice
   {
     int S = carry, mb = base.y, ri = base.x;
     for (int j = j0; j < j1; ++j) {
-      const int v = ids[j];
+      const int v = id(j);
       if (v >= 0 && (j == 0 || ids[j - 1] != v)) S = j;
-      if (v >= 0 && (j == nblk - 1 || ids[j + 1] != v)) {
+      if (v >= 0 && (j == nblk - 1 || id(j + 1) != ids[j])) {
         const int z = zv[j];
         const int nt = tiles_of(z);
         const int P = mb * ntn, Pe = (mb + nt) * ntn;

@@ -92,3 +92,50 @@ def test_all_three_kernels_give_the_same_bits():
         assert same_bits(run(lo, lo + 8), whole[lo * 128:(lo + 8) * 128]), lo
     for b in range(0, blocks, 5):
         assert same_bits(run(b, b + 1), whole[b * 128:(b + 1) * 128]), b
+
+
+# valid rows of consecutive 128-row blocks and their experts: blocks that are not full
+# in the middle of an expert's, half blocks, empty ones
+_ROWS = [3, 128, 128, 64, 0, 127, 128, 1, 128, 128, 65, 128, 0, 128, 100, 77]
+_IDS = [0, 0, 0, 0, 0, 1, 1, 1, 1, 0, 0, 2, 2, 2, 2, 2]
+
+
+@pytest.mark.parametrize("times,K,cut,tile", [(1, 4096, 0, "256"), (1, 4096, 30, "256"), (40, 512, 51, "256"),
+                                              (1, 1408, 0, "128"), (1, 1408, 51, "128"), (1, 256, 0, "64"), (1, 256, 51, "64")])
+def test_blocks_that_are_not_full(times, K, cut, tile):
+    """Padding rows inside an expert's blocks hold NaN and are neither read into a row
+    nor written, whichever kernel takes the call; the last block may be cut."""
+    announce("dgrad partial blocks", times, K, cut)
+    N = 256
+    m = np.full(16 * times * 128, -1, np.int32)
+    for b in range(16 * times):
+        m[b * 128:b * 128 + _ROWS[b % 16]] = _IDS[b % 16]
+    m = m[:len(m) - cut]
+    assert _kernel(len(m), K) == tile
+    dC, B = _ints(-1, 2, len(m), N), _ints(-1, 3, 3, N, K)
+    named = torch.from_numpy(m >= 0).to(DEV)
+    dC[~named] = float("nan")
+    dA = poison((len(m), K), BF)
+    before = dA.clone()
+    L.grouped_gemm_contig_dgrad(dC, B, dA, i32_dev(m))
+    for e in range(3):
+        at = torch.from_numpy(m == e).to(DEV)
+        assert torch.equal(dA[at].float(), (dC[at].float() @ B[e].float()).to(BF).float()), e
+    assert same_bits(dA[~named], before[~named])
+
+
+def test_as_many_runs_as_blocks():
+    """8160 blocks of one row each: every XCD's share of the run table is full."""
+    announce("dgrad 8160 runs")
+    N, K, blocks = 128, 256, 8160
+    m = np.full(blocks * 128, -1, np.int32)
+    m[::128] = np.arange(blocks) // 4000
+    rows = torch.arange(0, blocks * 128, 128, device=DEV)
+    dC, B = torch.full((blocks * 128, N), float("nan"), dtype=BF, device=DEV), _ints(-1, 3, 3, N, K)
+    dC[rows] = _ints(-1, 2, blocks, N)
+    dA = poison((blocks * 128, K), BF)
+    L.grouped_gemm_contig_dgrad(dC, B, dA, i32_dev(m))
+    want = torch.bmm(dC[rows].float()[:, None], B.float()[rows // 128 // 4000])[:, 0]
+    assert torch.equal(dA[rows].float(), want.to(BF).float())
+    dA[rows] = poison((1, K), BF)
+    assert torch.equal(dA.view(torch.int16), poison((blocks * 128, K), BF).view(torch.int16))

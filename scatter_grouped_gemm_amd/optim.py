@@ -8,6 +8,8 @@ gradient scale live on the device and are read by the kernel.
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import _lib as L
@@ -48,8 +50,8 @@ class AdamW:
         wd = [float(weight_decay)] * len(params) if isinstance(weight_decay, (int, float)) else list(weight_decay)
         if len(wd) != len(params):
             raise ValueError(f"{len(params)} parameters and {len(wd)} weight decays")
-        if not (0.0 <= betas[0] < 1.0 and 0.0 <= betas[1] < 1.0) or not eps > 0.0:
-            raise ValueError("betas lie in [0, 1) and eps is positive")
+        if not (0.0 <= betas[0] < 1.0 and 0.0 <= betas[1] < 1.0) or not ctypes.c_float(eps).value > 0.0:
+            raise ValueError("betas lie in [0, 1) and eps is positive (in fp32)")
         dev = params[0].device
         code = {torch.bfloat16: L.MOE_DTYPE_BF16, torch.float32: L.MOE_DTYPE_FP32}
         for i, (p, g) in enumerate(zip(params, grads)):

@@ -6,7 +6,7 @@ import torch
 from scatter_grouped_gemm_amd import AdamW
 from scatter_grouped_gemm_amd import _lib as L
 from gpu_util import DEV, announce
-from test_gpu_training import BF, F32, _make, gen, randn, same_bits
+from test_gpu_training import BF, F32, U32, _make, gen, randn, same_bits, within
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +77,20 @@ def test_accumulating_over_replays_and_small_batches():
         graph.replay()
         torch.cuda.synchronize()
     assert layer.dw13.any() and same_bits(layer.dw13, eager.dw13) and same_bits(layer.dw2, eager.dw2)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-45, 1e-40, 1.5e-38, 1e-37])
+def test_adamw_with_the_smallest_eps(eps, bits):
+    """Weights without a gradient stay as they were, the others move by lr: the first
+    step's m / (1 - b1) is the gradient and its root of v / (1 - b2) its magnitude."""
+    announce("adamw eps", eps, bits)
+    lr = 0.01
+    w, g = randn(1, 6000, dtype=F32), randn(2, 6000, dtype=F32)
+    g[::3] = 0
+    g[2048:4096] = 0                                         # whole groups too
+    p = w.to(DEV)
+    AdamW([p], [g.to(DEV)], lr=lr, betas=(0.9, 0.99), eps=eps, state_bits=bits).step()
+    assert same_bits(p.cpu()[g == 0], w[g == 0])
+    # constants, products, root and quotient of a step as in the bound of the plain step's test
+    within(p, w.double() - lr * torch.sign(g.double()), 3 * U32 * w.double().abs() + 24 * U32 * lr)

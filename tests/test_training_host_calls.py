@@ -61,3 +61,10 @@ def test_gradients_are_allocated_once():
     b.fill_(1)
     layer.allocate_grads()
     assert layer.dw13 is a and layer.dw2 is b and not a.any() and not b.any()
+
+
+def test_adamw_refuses_an_eps_that_is_zero_in_fp32():
+    for eps in (1e-46, 1e-300, float("nan"), -1e-8):
+        with pytest.raises(ValueError, match="eps"):
+            AdamW([torch.zeros(8)], [torch.zeros(8)], eps=eps)
+    AdamW([torch.zeros(8)], [torch.zeros(8)], eps=1e-45)     # the smallest fp32 number

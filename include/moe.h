@@ -512,8 +512,9 @@ int32_t moe_adamw_plan(const moe_adamw_tensor* tensors, int32_t n, void* host_pl
  * is cut to e4m3 after adding 16 random bits below its last place (so its
  * expectation is x; a positive root of v never becomes 0).  The bits are a hash of (seed, t, tensor's place in the
  * plan, element): the same call on the same state gives the same result.
- *   plan       device copy of the plan, plan_bytes its size, 16-byte aligned; the
- *              tensors of a plan that is cut short stay as they are
+ *   plan       device copy of the plan, plan_bytes its size, 16-byte aligned; with
+ *              a plan that is cut short the call does nothing: tensors and
+ *              counter stay as they are
  *   lr         device fp32 [1], grad_scale device fp32 [1] or NULL (1): read by
  *              the kernel, so a captured step follows them
  *   counter    device int64 [2]: the number of steps taken (>= 0), and 0.  The

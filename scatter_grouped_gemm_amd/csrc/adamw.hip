@@ -174,7 +174,7 @@ __global__ __launch_bounds__(256, 8) void adamw_kernel(const uint8_t* __restrict
   const Header* const h = reinterpret_cast<const Header*>(plan);
   const moe_adamw_tensor* const tensors = reinterpret_cast<const moe_adamw_tensor*>(plan + sizeof(Header));
   const int2* const chunks = reinterpret_cast<const int2*>(tensors + h->tensors);
-  // a plan cut short lists nothing
+  // a plan cut short lists nothing, and its call is no step
   const bool whole = h->magic == kMagic && sizeof(Header) + h->tensors * sizeof(moe_adamw_tensor) +
                                                    h->chunks * sizeof(int2) <= plan_bytes;
   const int nchunk = whole ? h->chunks : 0;
@@ -267,7 +267,7 @@ __global__ __launch_bounds__(256, 8) void adamw_kernel(const uint8_t* __restrict
   if (threadIdx.x == 0) {
     const unsigned long long ticket = atomicAdd(reinterpret_cast<unsigned long long*>(counter + 1), 1ull);
     if (ticket == gridDim.x - 1) {
-      counter[0] = step;
+      if (whole) counter[0] = step;
       counter[1] = 0;
     }
   }

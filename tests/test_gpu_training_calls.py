@@ -94,3 +94,23 @@ def test_adamw_with_the_smallest_eps(eps, bits):
     assert same_bits(p.cpu()[g == 0], w[g == 0])
     # constants, products, root and quotient of a step as in the bound of the plain step's test
     within(p, w.double() - lr * torch.sign(g.double()), 3 * U32 * w.double().abs() + 24 * U32 * lr)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_plan_cut_short_counts_no_step(bits):
+    """The step behind such calls is the first one: its bias corrections and random
+    bits are those of a fresh optimizer."""
+    announce("adamw plan cut counts", bits)
+    p = randn(1, 5000, dtype=F32).to(DEV)
+    q, g = p.clone(), randn(2, 5000, dtype=F32).to(DEV)
+    o, fresh = AdamW([p], [g], state_bits=bits, seed=3), AdamW([q], [g], state_bits=bits, seed=3)
+    whole = o._plan
+    for cut in (8, 16, 80):
+        L.moe_adamw_step(whole[:-cut].contiguous(), o.lr, o._counter, 0.9, 0.95, 1e-8)
+    other = whole.clone()
+    other[0] += 1                                            # not a plan
+    L.moe_adamw_step(other, o.lr, o._counter, 0.9, 0.95, 1e-8)
+    assert o._counter.tolist() == [0, 0]
+    o.step(), fresh.step()
+    assert o._counter.tolist() == [1, 0]
+    assert same_bits(p, q) and same_bits(o.m, fresh.m) and same_bits(o.v, fresh.v)

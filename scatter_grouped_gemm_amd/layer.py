@@ -187,6 +187,7 @@ class MoELayer:
         T = x.shape[0]
         if T > self.T_max:
             raise ValueError(f"{T} tokens exceed the layer's static capacity {self.T_max}")
+        self._saved = None       # from here on the buffers are no longer the last forward's
         if topk_ids is None:
             with self._mark("route"):
                 self.route(logits)
@@ -266,8 +267,8 @@ class MoELayer:
 
         With a share of the experts, dx and dlogits are that share's part: both
         add up over the shares.  What forward kept is used up: one backward for
-        each forward, and ids and weights given to forward must still be as
-        they were."""
+        each forward that came to its end, and ids and weights given to forward
+        must still be as they were."""
         if not self.train:
             raise ValueError("the layer was made without train=True")
         if self._saved is None:

@@ -114,3 +114,34 @@ def test_a_plan_cut_short_counts_no_step(bits):
     o.step(), fresh.step()
     assert o._counter.tolist() == [1, 0]
     assert same_bits(p, q) and same_bits(o.m, fresh.m) and same_bits(o.v, fresh.v)
+
+
+def test_backward_behind_a_forward_that_failed_is_refused():
+    announce("layer forward that fails")
+    layer, x, logits, _, _ = _make(16, 256, 128, 4, 2)
+    xd, dout = x.to(DEV), randn(1, 16, 256).to(DEV)
+    layer(xd, logits.to(DEV))
+    ids = torch.zeros(8, 2, dtype=torch.int32, device=DEV)
+    with pytest.raises(AssertionError):                      # the weights are not on the device: fails in the combine
+        layer(xd[:8], topk_ids=ids, topk_weights=torch.ones(8, 2))
+    with pytest.raises(ValueError, match="forward"):
+        layer.backward(dout)
+    layer(xd, logits.to(DEV))
+    layer.backward(dout)
+
+
+def test_an_empty_batch_through_the_layer():
+    """No rows behind a batch with rows: its gradients are zero, or what they were."""
+    announce("layer empty batch")
+    layer, x, logits, _, _ = _make(16, 256, 128, 4, 2)
+    xd, ld, dout = x.to(DEV), logits.to(DEV), randn(1, 16, 256).to(DEV)
+    layer(xd, ld)
+    layer.backward(dout)
+    had = layer.dw13.clone()
+    layer(xd[:0], ld[:0])
+    layer.backward(dout[:0], accumulate=True)
+    assert had.any() and same_bits(layer.dw13, had)
+    out = layer(xd[:0], ld[:0])
+    dx, dl = layer.backward(dout[:0])
+    assert out.shape == dx.shape == (0, 256) and dl.shape == (0, 4)
+    assert not layer.dw13.any() and not layer.dw2.any()

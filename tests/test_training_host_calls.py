@@ -68,3 +68,16 @@ def test_adamw_refuses_an_eps_that_is_zero_in_fp32():
         with pytest.raises(ValueError, match="eps"):
             AdamW([torch.zeros(8)], [torch.zeros(8)], eps=eps)
     AdamW([torch.zeros(8)], [torch.zeros(8)], eps=1e-45)     # the smallest fp32 number
+
+
+def test_a_forward_that_fails_leaves_nothing_for_backward():
+    """Its first calls have overwritten what the forward before it had left."""
+    layer = MoELayer(num_experts=4, top_k=2, hidden=128, intermediate=128, max_tokens=8, train=True, device="cpu")
+    before = layer._saved = (8, layer.topk_ids, layer.topk_weights, True)
+    with pytest.raises(ValueError, match="capacity"):         # refused before anything is written
+        layer(torch.zeros(9, 128, dtype=torch.bfloat16), torch.zeros(9, 4))
+    assert layer._saved is before
+    with pytest.raises(AssertionError):                       # not on the device
+        layer(torch.zeros(8, 128, dtype=torch.bfloat16), torch.zeros(8, 4))
+    with pytest.raises(ValueError, match="forward"):
+        layer.backward(torch.zeros(8, 128, dtype=torch.bfloat16))

@@ -449,6 +449,16 @@ def grouped_gemm_contig_wgrad(dC, A, expert_start_loc, num_valid, dB, accumulate
         _dev("dB", dB.dtype, (G, N, K), dB, dev), M, N, K, G, _raw_stream(dev)))
 
 
+def grouped_gemm_grads_supported(M: int, N: int, K: int, G: int) -> bool:
+    """Whether the two gradient products cover these sizes (their limits are the
+    same).  Host only: the call checks sizes before pointers, and without pointers
+    it ends there."""
+    if not all(0 <= x < 1 << 31 for x in (M, N, K, G)):
+        return False
+    st = lib().grouped_gemm_contig_wgrad(None, None, None, None, MOE_DTYPE_BF16, 0, None, M, N, K, G, None)
+    return st == MOE_EINVAL and N > 0 and K > 0 and G > 0
+
+
 def moe_adamw_plan(tensors) -> torch.Tensor:
     """Host plan (uint8 tensor) of a list of AdamwTensor; copy it to the device."""
     arr = (AdamwTensor * len(tensors))(*tensors)

@@ -20,7 +20,8 @@ Training (``train=True``, BF16 weights, compact layout): forward keeps what the
 gradients need in its own buffers and backward(dout) walks the same steps back --
 combine, w2 (weight, then input), SiLU-and-mul, w13 (weight, then input),
 scatter -- with no further host work; optimizer() gives the AdamW step over the
-expert weights.
+expert weights.  The gradient products end at 1,044,480 rows (8160 blocks of 128);
+a training layer with more is refused.
 """
 from __future__ import annotations
 
@@ -81,6 +82,10 @@ class MoELayer:
         else:
             self.rows = El * self.max_m
         R = self.rows
+        if train:        # before any memory is taken: forward alone runs with more rows
+            for n, kk in ((2 * I, H), (H, I)):
+                if not L.grouped_gemm_grads_supported(R, n, kk, El):
+                    raise ValueError(f"training: the gradient products do not cover {R} rows, {El} experts of {n} x {kk}")
         adt = torch.uint8 if fp8 else torch.bfloat16
         # static buffers (uninitialised: every valid row is written before it is read)
         self.topk_ids = torch.empty(T, k, dtype=torch.int32, device=d)

@@ -81,3 +81,24 @@ def test_a_forward_that_fails_leaves_nothing_for_backward():
         layer(torch.zeros(8, 128, dtype=torch.bfloat16), torch.zeros(8, 4))
     with pytest.raises(ValueError, match="forward"):
         layer.backward(torch.zeros(8, 128, dtype=torch.bfloat16))
+
+
+def test_a_layer_that_backward_could_not_serve_is_refused():
+    """Past 8160 blocks of 128 rows forward still runs, the gradient products do not;
+    nor do they with other sizes past their limits."""
+    make = lambda train=True, **kw: MoELayer(**{**dict(num_experts=4, top_k=2, hidden=128, intermediate=128,  # noqa: E731
+                                                       max_tokens=8, train=train, device="meta"), **kw})
+    most = 8160 * 128
+    rows = lambda T: L.moe_compact_rows_bound(2 * T, 4, 128)  # noqa: E731
+    T = max(t for t in range(most // 2 - 400, most // 2) if rows(t) <= most)
+    assert rows(T + 64) > most
+    assert make(max_tokens=T).rows <= most
+    for kw in (dict(max_tokens=T + 64), dict(hidden=4194304 + 128), dict(intermediate=4194304), dict(hidden=192),
+               dict(num_experts=1025)):
+        with pytest.raises(ValueError, match="gradient products"):
+            make(**kw)
+    assert make(train=False, layout="compact", max_tokens=T + 64).rows > most
+    for sizes, want in [((0, 128, 128, 1), True), ((most, 128, 128, 1024), True), ((most + 1, 128, 128, 1), False),
+                        ((128, 64, 128, 1), False), ((128, 128, 128, 0), False), ((1 << 40, 128, 128, 1), False),
+                        ((-1, 128, 128, 1), False)]:
+        assert L.grouped_gemm_grads_supported(*sizes) is want, sizes

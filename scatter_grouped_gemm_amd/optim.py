@@ -35,7 +35,8 @@ class AdamW:
     ``v_scale``) are flat over all tensors, tensor i at ``offsets[i]``, a
     multiple of 128; ``v`` holds the codes of its root where state_bits is 8.
     ``state_dict`` gives what a checkpoint has to keep (and the fp32 parameters,
-    which are the caller's).
+    which are the caller's), the seed among it: a run that is taken up again rounds
+    as it would have.
     """
 
     def __init__(self, params, grads, *, lr: float = 1e-3, betas=(0.9, 0.95), eps: float = 1e-8,
@@ -109,20 +110,27 @@ class AdamW:
     def state_dict(self) -> dict:
         """The state's tensors (not copies): what a checkpoint has to keep."""
         names = ("master", "m", "v", "m_scale", "v_scale", "lr")
-        return {"steps": self.steps, "offsets": list(self.offsets), "state_bits": self.state_bits,
+        return {"steps": self.steps, "offsets": list(self.offsets), "state_bits": self.state_bits, "seed": self.seed,
                 **{n: getattr(self, n) for n in names if getattr(self, n) is not None}}
 
     @torch.no_grad()
     def load_state_dict(self, state: dict):
-        """Take over another run's state_dict (same tensors, same state_bits); bf16
-        parameters become their masters' roundings."""
+        """Take over another run's state_dict (same tensors, same state_bits) and its
+        seed (this one's stays if it holds none); bf16 parameters become their
+        masters' roundings.  A step captured before keeps the seed it was captured
+        with: capture it again if they differ."""
         mine = self.state_dict()
+        seed = state.get("seed", self.seed)
+        if not isinstance(seed, int):
+            raise ValueError(f"seed: want a whole number, got {seed!r}")
+        state = {**state, "seed": seed}
         if state.keys() != mine.keys() or state["state_bits"] != self.state_bits or list(state["offsets"]) != self.offsets:
             raise ValueError("the state is of other tensors or another state_bits")
         for n, t in mine.items():
             if isinstance(t, torch.Tensor):
                 if state[n].shape != t.shape or state[n].dtype != t.dtype:
                     raise ValueError(f"{n}: want {t.dtype} {tuple(t.shape)}, got {state[n].dtype} {tuple(state[n].shape)}")
+        self.seed = seed
         for n, t in mine.items():
             if isinstance(t, torch.Tensor):
                 t.copy_(state[n])

@@ -145,3 +145,15 @@ def test_an_empty_batch_through_the_layer():
     dx, dl = layer.backward(dout[:0])
     assert out.shape == dx.shape == (0, 256) and dl.shape == (0, 4)
     assert not layer.dw13.any() and not layer.dw2.any()
+
+
+def test_adamw_resumed_in_an_optimizer_of_another_seed():
+    announce("adamw resume seed")
+    g = randn(1, 5000).to(DEV)
+    a = randn(2, 5000).to(DEV)
+    b = torch.zeros_like(a)
+    o, n = (AdamW([p], [g], lr=1e-2, state_bits=8, seed=seed) for p, seed in ((a, 4), (b, 9)))
+    o.step(), o.step()
+    n.load_state_dict({k: v.clone() if isinstance(v, torch.Tensor) else v for k, v in o.state_dict().items()})
+    o.step(), n.step()
+    assert same_bits(a, b) and same_bits(o.m, n.m) and same_bits(o.v, n.v)

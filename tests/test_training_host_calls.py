@@ -102,3 +102,20 @@ def test_a_layer_that_backward_could_not_serve_is_refused():
                         ((128, 64, 128, 1), False), ((128, 128, 128, 0), False), ((1 << 40, 128, 128, 1), False),
                         ((-1, 128, 128, 1), False)]:
         assert L.grouped_gemm_grads_supported(*sizes) is want, sizes
+
+
+def test_adamw_state_holds_the_seed():
+    make = lambda seed: AdamW([torch.zeros(130)], [torch.zeros(130)], state_bits=8, seed=seed)  # noqa: E731
+    saved = make(5).state_dict()
+    assert saved["seed"] == 5
+    o = make(7)
+    with pytest.raises(ValueError):
+        o.load_state_dict({**saved, "state_bits": 32})
+    with pytest.raises(ValueError, match="seed"):
+        o.load_state_dict({**saved, "seed": None})
+    assert o.seed == 7                                        # nothing was taken over
+    o.load_state_dict(saved)
+    assert o.seed == 5
+    o = make(7)
+    o.load_state_dict({k: v for k, v in saved.items() if k != "seed"})   # saved without one
+    assert o.seed == 7

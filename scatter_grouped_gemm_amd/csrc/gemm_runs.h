@@ -157,7 +157,7 @@ struct Share {
 // FULL: the rows of a run are all valid (a block whose last row is not ends it);
 // otherwise only its last block's are counted, and the padding of an earlier one
 // is taken for rows of the run.  It reads that row of every block too: 6400 blocks,
-// N and K 256 218 us, 209 without; up to 600 blocks no difference.
+// N and K 256 216 us, 209 without; up to 600 blocks no difference.
 // Every run has a tile, and a share no more tiles than an eighth of the blocks
 // and two, so kTable entries hold the runs of either kind.
 constexpr int kPartial = 1 << 16;  // in ids: the block is not full (ids are below 1024 then)
@@ -169,7 +169,6 @@ __device__ __forceinline__ bool build_share(const int32_t* __restrict__ m_indice
   const int tid = threadIdx.x;
   const int nblk = static_cast<int>((M + 127) / 128);
   if constexpr (FULL) {
-#pragma unroll 4
     for (int j = tid; j < nblk; j += kThreads) {
       const int32_t* const b = m_indices + static_cast<int64_t>(j) * 128;
       const int v = b[0], end = b[j + 1 < nblk ? 127 : 0];  // both loads in flight together

@@ -493,7 +493,8 @@ typedef struct {
   int32_t state_bits;
 } moe_adamw_tensor;
 
-/* Host: bytes of the plan for n tensors, 0 where they are invalid. */
+/* Host: bytes of the plan for n tensors, 0 where they are invalid.  Limit: fewer
+ * than 2^31 pieces of 2048 elements over all tensors. */
 size_t moe_adamw_plan_bytes(const moe_adamw_tensor* tensors, int32_t n);
 
 /* Host: writes the plan of n tensors to host_plan.  The caller copies its

@@ -291,6 +291,8 @@ int32_t check(const moe_adamw_tensor* t, int32_t n, int64_t* chunks) {
     if (d.state_bits == 8 && (!d.m_scale || !d.v_scale)) return MOE_EINVAL;
     if (!aligned16(d.param) || !aligned16(d.grad) || !aligned16(d.m) || !aligned16(d.v)) return MOE_EUNSUPPORTED;
     if (d.param_dtype == MOE_DTYPE_BF16 && !aligned16(d.master)) return MOE_EUNSUPPORTED;
+    // compared before it is added: neither sum passes 64 bits
+    if (d.numel > static_cast<int64_t>(INT32_MAX) * kChunk) return MOE_EUNSUPPORTED;
     total += (d.numel + kChunk - 1) / kChunk;
     if (total > INT32_MAX) return MOE_EUNSUPPORTED;
   }

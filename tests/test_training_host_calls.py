@@ -119,3 +119,13 @@ def test_adamw_state_holds_the_seed():
     o = make(7)
     o.load_state_dict({k: v for k, v in saved.items() if k != "seed"})   # saved without one
     assert o.seed == 7
+
+
+@pytest.mark.parametrize("numel", [(1 << 63) - 1, (1 << 63) - 2047, 1 << 62, (1 << 31) * 2048, ((1 << 31) - 1) * 2048 + 1])
+def test_adamw_plan_refuses_tensors_past_its_pieces(numel):
+    """Also where rounding such a size up would pass 64 bits."""
+    t = dict(param=P, grad=P, m=P, v=P, param_dtype=L.MOE_DTYPE_FP32, grad_dtype=L.MOE_DTYPE_FP32, state_bits=32)
+    for arr in ([dict(numel=numel)], [dict(numel=5000), dict(numel=numel)], [dict(numel=((1 << 31) - 1) * 2048), dict(numel=1)]):
+        ts = (L.AdamwTensor * len(arr))(*[L.AdamwTensor(**t, **a) for a in arr])
+        assert L.lib().moe_adamw_plan_bytes(ts, len(arr)) == 0
+        assert L.lib().moe_adamw_plan(ts, len(arr), None, 1 << 40) == L.MOE_EUNSUPPORTED

@@ -128,6 +128,8 @@ class MoELayer:
     # -- weights ---------------------------------------------------------------------
 
     def allocate_weights(self):
+        if self.train and self.w13 is not None:      # an optimizer may hold them
+            return
         d, El, H, I = self.device, self.El, self.H, self.I
         wdt = torch.uint8 if self.fp8 else torch.bfloat16
         half = 2 if self.weight_format == "mxfp4" else 1      # e2m1: two k per byte

@@ -129,3 +129,18 @@ def test_adamw_plan_refuses_tensors_past_its_pieces(numel):
         ts = (L.AdamwTensor * len(arr))(*[L.AdamwTensor(**t, **a) for a in arr])
         assert L.lib().moe_adamw_plan_bytes(ts, len(arr)) == 0
         assert L.lib().moe_adamw_plan(ts, len(arr), None, 1 << 40) == L.MOE_EUNSUPPORTED
+
+
+def test_weights_of_a_training_layer_are_allocated_once():
+    """An optimizer that holds them would go on updating the old ones."""
+    make = lambda train: MoELayer(num_experts=4, top_k=2, hidden=128, intermediate=128, max_tokens=8, train=train, device="cpu")  # noqa: E731
+    layer = make(True)
+    layer.set_weights(torch.ones(4, 256, 128), torch.ones(4, 128, 128))
+    opt = layer.optimizer()
+    layer.allocate_weights()
+    assert opt.params[0] is layer.w13 and opt.params[1] is layer.w2 and (layer.w13 == 1).all()
+    other = make(False)
+    other.allocate_weights()
+    w13 = other.w13
+    other.allocate_weights()
+    assert other.w13 is not w13

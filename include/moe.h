@@ -477,7 +477,9 @@ int32_t grouped_gemm_contig_wgrad(const void* dC, const void* A, const int32_t* 
  *                 rounded up to 128: the e4m3 codes of m and of the root of v
  *   m_scale, v_scale  state_bits 8: device u8 [ceil(numel / 128)], the UE8M0
  *                 scale of each 128 elements; else NULL
- *   weight_decay  of this tensor */
+ *   weight_decay  of this tensor
+ * No param, master, m, v or scale may overlap another tensor of the plan or a
+ * gradient; gradients may overlap each other. */
 typedef struct {
   void* param;
   float* master;

@@ -8,6 +8,7 @@ gradient scale live on the device and are read by the kernel.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 
 import torch
@@ -22,7 +23,7 @@ class AdamW:
 
     params, grads    lists of contiguous tensors of equal sizes on one device,
                      16-byte aligned; params bf16 or fp32, none overlapping
-                     another, grads bf16 or fp32.  A
+                     another or a gradient; grads bf16 or fp32.  A
                      bf16 parameter is the rounding of an fp32 master that this
                      class holds; both stay where they are between steps (write
                      new gradients into the same buffers).
@@ -71,6 +72,15 @@ class AdamW:
         for (_, end, i), (start, _, j) in zip(held, held[1:]):
             if start < end:          # two updates of one element would race
                 raise ValueError(f"parameters {i} and {j} share memory")
+        starts = [h[0] for h in held]
+        for j, g in enumerate(grads):
+            lo = g.data_ptr()
+            hi = lo + g.numel() * g.element_size()
+            k = bisect.bisect_left(starts, hi) - 1       # the last parameter that begins before its end
+            if g.numel() and k >= 0 and held[k][1] > lo and held[k] != (lo, hi, j):
+                # read by one workgroup while another writes (its own parameter itself is
+                # read and written by the same lanes)
+                raise ValueError(f"gradient {j} and parameter {held[k][2]} share memory")
         self.params, self.grads = params, grads
         self.betas, self.eps, self.seed, self.state_bits = (float(betas[0]), float(betas[1])), float(eps), int(seed), state_bits
         self.offsets, total = [], 0

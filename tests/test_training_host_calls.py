@@ -144,3 +144,16 @@ def test_weights_of_a_training_layer_are_allocated_once():
     w13 = other.w13
     other.allocate_weights()
     assert other.w13 is not w13
+
+
+def test_adamw_refuses_gradients_in_a_parameters_memory():
+    """One workgroup would read what another writes."""
+    a, b = torch.zeros(512), torch.zeros(512)
+    for params, grads in [([a], [a.view(torch.bfloat16)[:512]]), ([a[:256]], [a[128:384]]), ([a[:256], b[:256]], [b[:256], b[256:]]),
+                          ([a[:4], b, a[256:]], [a[64:68], b.clone(), a[128:384]]), ([a[:256]], [a[252:508]])]:
+        with pytest.raises(ValueError, match="share"):
+            AdamW(params, grads)
+    AdamW([a[:256]], [a[256:]])                               # beside it
+    AdamW([a[:4], b, a[256:]], [a[64:68], b.clone(), b[:256].clone()])
+    AdamW([a[:0], a], [a[:0], b])
+    AdamW([a], [a])                                           # read and written by the same lanes

@@ -512,9 +512,13 @@ int32_t moe_adamw_plan(const moe_adamw_tensor* tensors, int32_t n, void* host_pl
  * (1 - beta^t in double).  The step uses m and v before they are rounded to 8
  * bits.  8-bit states: for each 128 elements e is the smallest integer in
  * [-126, 127] with amax <= 448 * 2^e; x * 2^-e (the power within one fp32 place)
- * is cut to e4m3 after adding 16 random bits below its last place (so its
- * expectation is x; a positive root of v never becomes 0).  The bits are a hash of (seed, t, tensor's place in the
- * plan, element): the same call on the same state gives the same result.
+ * is cut to e4m3 after adding 16 random bits below its last place, so its
+ * expectation is x (a positive root of v never becomes 0).  v, the root's square,
+ * is higher than its formula by the variance of that: it settles 2% above at beta2
+ * = 0.95 and 4% at 0.999 with normally distributed gradients (7% with sparse ones),
+ * and the steps come out half as much short.  The bits are a hash of (seed, t,
+ * tensor's place in the plan, element): the same call on the same state gives the
+ * same result.
  *   plan       device copy of the plan, plan_bytes its size, 16-byte aligned; with
  *              a plan that is cut short the call does nothing: tensors and
  *              counter stay as they are

@@ -12,7 +12,13 @@
 // small m into a step of m / eps).  Both are rounded up with the probability
 // of the remainder: a step moves v by a factor of at most 1 - b2 (0.1% at b2 =
 // 0.999), far less than the 6-12% between codes, so rounding to nearest would
-// leave v where it is for good; this way its expectation follows the formula.
+// leave v where it is for good.  This way the expectation of m and of the root
+// is what the formula gives.  That of v, the root's square, is higher by the
+// root's variance f (1 - f) u^2 (f the remainder in units u of the last place),
+// and the next step goes on from there: with normally distributed gradients v
+// settles 2% above its mean at b2 = 0.95 and 4% at 0.999 (3% and 7% where nine
+// in ten gradients are zero; never by more than an eighth of the mean of
+// |g^2 - v|), and the steps come out half as much short.
 // The random bits are a hash of (seed, step, tensor, element), so a step is
 // reproducible and needs no generator state.
 //

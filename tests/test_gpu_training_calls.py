@@ -157,3 +157,34 @@ def test_adamw_resumed_in_an_optimizer_of_another_seed():
     n.load_state_dict({k: v.clone() if isinstance(v, torch.Tensor) else v for k, v in o.state_dict().items()})
     o.step(), n.step()
     assert same_bits(a, b) and same_bits(o.m, n.m) and same_bits(o.v, n.v)
+
+
+@pytest.mark.parametrize("beta2,steps", [(0.95, 150), (0.999, 400)])
+def test_adamw_8bit_second_moment_over_many_steps(beta2, steps):
+    """The kernel's v against the formula in 64 bits: above it by what the root's variance
+    adds at each step, and by nothing else."""
+    announce("adamw many steps", beta2, steps)
+    n = 1 << 20
+    g = torch.ones(n, device=DEV)
+    o = AdamW([torch.zeros(n, device=DEV)], [g], betas=(0.9, beta2), state_bits=8, seed=2)
+    scale_of = lambda: torch.exp2(o.v_scale.double() - 127).repeat_interleave(128)  # noqa: E731
+    dg = torch.Generator(device=DEV)
+    dg.manual_seed(4)
+    v, mean = torch.zeros(n, dtype=torch.float64, device=DEV), torch.zeros(n, dtype=torch.float64, device=DEV)
+    gained = noise = 0.0
+    for _ in range(steps):
+        g.normal_(generator=dg)
+        o.step()
+        g2 = g.double() ** 2
+        want = beta2 * v + (1 - beta2) * g2
+        root, scale = want.sqrt(), scale_of()
+        unit = torch.exp2(torch.floor(torch.log2(root / scale)).clamp(min=-6) - 3) * scale
+        f = root / unit - torch.floor(root / unit)
+        spread = f * (1 - f) * unit ** 2
+        gained = beta2 * gained + spread.mean().item()
+        noise = beta2 ** 2 * noise + ((2 * root + unit) ** 2 * spread).mean().item() / n
+        v, mean = (o.v.view(torch.float8_e4m3fn).double() * scale) ** 2, beta2 * mean + (1 - beta2) * g2
+    over = (v.mean() - mean.mean()).item()
+    # six standard deviations; 16 random bits carry up to 2^-16 too seldom, which takes
+    # 2 r u 2^-16 <= v 2^-18 at a step, fp32 some v 2^-22; the mean of v is below 1.25
+    assert 0 < gained and abs(over - gained) <= 6 * noise ** 0.5 + steps * 1.25 * (2.0 ** -18 + 2.0 ** -22)

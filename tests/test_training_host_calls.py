@@ -157,3 +157,41 @@ def test_adamw_refuses_gradients_in_a_parameters_memory():
     AdamW([a[:4], b, a[256:]], [a[64:68], b.clone(), b[:256].clone()])
     AdamW([a[:0], a], [a[:0], b])
     AdamW([a], [a])                                           # read and written by the same lanes
+
+
+@pytest.mark.parametrize("beta2,steps", [(0.95, 300), (0.999, 2000)])
+def test_the_8bit_second_moment_over_many_steps(beta2, steps):
+    """The decoded v against the formula in 64 bits, with the format's rounding in plain
+    torch: the root's expectation is kept, so v gains the root's variance f (1 - f) u^2 at
+    each step.  With d = |v' - v| / (r' + r) the way that a step moves the root, r being a
+    code, f (1 - f) u <= d, and u <= r' / 8: all in all at most an eighth of |g^2 - v|."""
+    from perf.operators import GROUP, _rounded
+    gen = torch.Generator().manual_seed(3)
+    n = 64 * GROUP
+
+    def held(v):
+        bits = torch.randint(0, 65536, (n,), generator=gen)
+        codes, e = _rounded(v.sqrt().float(), bits, keep=True)
+        unit = torch.exp2(e.double() - 127).repeat_interleave(GROUP)
+        return codes.view(torch.float8_e4m3fn).double() * unit, unit
+
+    v, mean = held(torch.ones(n, dtype=torch.float64))[0] ** 2, torch.ones(n, dtype=torch.float64)
+    gained = noise = 0.0                  # of the mean over the elements: expectation and variance
+    most = 0.0
+    for _ in range(steps):
+        g2 = torch.randn(n, generator=gen, dtype=torch.float64) ** 2
+        most = max(most, (g2 - v).abs().mean().item())
+        want = beta2 * v + (1 - beta2) * g2
+        root = want.sqrt()
+        got, scale = held(want)
+        unit = torch.exp2(torch.floor(torch.log2(root / scale)).clamp(min=-6) - 3) * scale
+        f = root / unit - torch.floor(root / unit)
+        spread = f * (1 - f) * unit ** 2
+        gained = beta2 * gained + spread.mean().item()
+        noise = beta2 ** 2 * noise + ((2 * root + unit) ** 2 * spread).mean().item() / n
+        v, mean = got ** 2, beta2 * mean + (1 - beta2) * g2
+    over = (v.mean() - mean.mean()).item()
+    # six standard deviations; 16 random bits carry up to 2^-16 too seldom, which takes
+    # 2 r u 2^-16 <= v 2^-18 at a step, fp32 some v 2^-22; the mean of v is below 1.25
+    assert abs(over - gained) <= 6 * noise ** 0.5 + steps * 1.25 * (2.0 ** -18 + 2.0 ** -22)
+    assert 0 < gained <= most / 8

@@ -4,8 +4,9 @@
 //   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2,
 //   p = p (1 - lr wd) - (lr / (1 - b1^t)) m / (sqrt(v) / sqrt(1 - b2^t) + eps).
 //
-// 8-bit states: groups of 128 elements share one UE8M0 scale (the smallest e
-// with amax <= 448 * 2^e, as everywhere in this library).  m is kept as e4m3,
+// 8-bit states: groups of 128 elements share one UE8M0 scale (2^e, e the smallest
+// with amax <= 448 * 2^e, as everywhere in this library; what differs here is the
+// reciprocal that a value is multiplied by, see the kernel).  m is kept as e4m3,
 // v as the e4m3 of its root: the root needs half the octaves, so a group may
 // mix gradients 2^17 apart before the small ones reach the last code, and a
 // positive root keeps at least that code (a root of zero would turn the next
@@ -48,6 +49,8 @@ struct Header {
 };
 static_assert(sizeof(Header) == 16 && sizeof(moe_adamw_tensor) == 80, "plan layout");
 
+// A 32-bit hash of shifts and products.  The factors are the first two 32-bit primes
+// of the xxHash specification (the first is 2^32 over the golden ratio, nearly).
 __device__ __forceinline__ uint32_t mix(uint32_t x) {
   x ^= x >> 16;
   x *= 0x9E3779B1u;
@@ -168,10 +171,11 @@ __global__ __launch_bounds__(256, 8) void adamw_kernel(const uint8_t* __restrict
                                                     const float* __restrict__ grad_scale,
                                                     int64_t* counter, double beta1, double beta2,
                                                     float eps, uint32_t seed) {
-  // The reciprocal of each scale, taken as powf(2, -e): within 2^-24 of 2^-e, and
-  // what a torch program that scales by a power multiplies by on this card.  What
-  // is cut at random does not mind its last place, and such a program gets the same
-  // codes, bit for bit.
+  // The reciprocal of each scale, taken as powf(2, -e): within 2^-24 of 2^-e (one place
+  // off for 41 of the 254 exponents), and what a torch program that scales by a power
+  // multiplies by on this card, so that such a program gets the same codes bit for bit.
+  // The exact power gives another code where the remainder and the random bits add up
+  // to 1 but for that place (one in half a million), and takes as long.
   __shared__ float inverse[256];
   float two = 2.0f;
   asm volatile("" : "+v"(two));  // as a constant it becomes exp2f, which is another function

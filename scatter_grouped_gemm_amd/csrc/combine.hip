@@ -7,7 +7,8 @@
 // it arrives in.
 // The gradient of the scatter is the same sum without weights (each copy of a
 // token passes its gradient back unchanged), so it is the same kernel with
-// WEIGHTED false (16384 tokens, H 4096, top-8: 219 us, 5.5 TB/s).
+// WEIGHTED false (16384 tokens, H 4096, top-8: 220 us, 5.5 TB/s; 4096 tokens, H 7168,
+// top-16 181 us, 5.5 TB/s, top-32 343 us, 5.6 TB/s).
 #include "common.h"
 
 namespace moe {

@@ -29,12 +29,16 @@
 // Where 256 x 256 tiles do not fill the card, or hold a few steps only, smaller
 // ones take the call: dgrad_thin_kernel below, dgrad_short.hip, wgrad_short.hip.
 //
-// Measured (TFLOP/s; in brackets torch's library product of one matrix with the same
-// layout): 4096 rows by 8192 by 4096 dgrad 186 us, 1480 (8192 rows: 1236-1390); 8
-// experts of 1024 rows, N 28672, K 4096 dgrad 1.34-1.49 ms, 1290-1440, wgrad
-// 1.65-1.75 ms, 1100-1160 (one of the experts alone 1004); one expert of 16384 rows,
-// 4096 x 4096 wgrad 390-410 us, 1340-1400 (997).  64 ragged experts (N 2816, K 2048,
-// 4662 rows) dgrad 141 us: B is read at 5.5 TB/s.
+// Measured (us; in brackets TFLOP/s; of one matrix also torch's library product of
+// the same sizes and layout, in turn):
+//   dgrad  4096 rows, N 8192, K 4096 185 (1488), library 198 (1390); 8192 rows 360
+//          (1528), 393 (1398); 8192 rows, N 28672 1266 (1520), 1382 (1392)
+//   wgrad  16384 rows, 4096 x 4096 403 (1365), 468 (1175); 8192 rows, 4096 x 8192 387
+//          (1422), 455 (1208); 1024 rows, 28672 x 4096 211 (1139), 247 (974)
+//   8 experts, N 28672, K 4096: of 1024 rows dgrad 1290-1490 (1290-1490), wgrad
+//          1650-1750 (1100-1160); of 964 to 1084 rows dgrad 1720-1740 (1110): 560 to 592
+//          tiles take three rounds of 256 workgroups, where 1024 rows take two
+//   64 ragged experts (N 2816, K 2048, 4662 rows) dgrad 138: B is read at 5.5 TB/s
 // What bounds them: dgrad the card's power (matrix cores busy 81% of the cycles at
 // 1.55 GHz); wgrad the load parts (busy 57-67% at 1.8 GHz: its P takes twice the
 // LDS instructions) and, with short reductions, the stores (without them the 8
@@ -428,7 +432,8 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grad_kernel(const GradArgs a
 // With few rows the product is one pass over B, and what counts is how many CUs
 // read it and how much each has in flight.  A 256-column tile of a B [8192][2048]
 // leaves 8 workgroups an expert, each reading 4 MB a step at a time: 133 us for
-// one token and two experts, where the bytes take 14.  Here four wavefronts of 16
+// one token and two experts, where the bytes take 14 (44 here: its 64 workgroups are
+// a quarter of the CUs).  Here four wavefronts of 16
 // columns each keep seven steps of 64 (56 KB of B) in flight in eight LDS stages
 // of 16 KB.  The sum of an output runs through the same MFMAs in the same order
 // as in the large kernel, so a row comes out the same from either.
@@ -586,6 +591,9 @@ int32_t launch(const GradArgs& a, void* stream) {
 //     experts, 4096 x 4096, 64 rows 78 / 86, added 119 / 131.)
 // Rows are M over G, which the host knows; rows dealt unevenly change little (64
 // experts, 2048 x 1408, fp32 added, 8192 rows in one and two in each other 401 / 363).
+// M is the buffers' height and not the rows held: in buffers that hold few, the wide
+// tiles take the call (2 of 64 experts with 32 rows each, 4096 x 2048, bf16: 14 us in
+// buffers of 256 rows, 22 in buffers of 2176).
 template <bool F32, bool ACC>
 int32_t launch_wgrad(const GradArgs& a, void* stream) {
   const int64_t tiles = static_cast<int64_t>(a.N / 128) * (a.K / 128) * a.G;
@@ -642,6 +650,9 @@ extern "C" int32_t grouped_gemm_contig_dgrad(const void* dC, const void* B, void
   //     395 / 259 / 266
   //   512 of 128 x 128:  N 4096, 2048 rows, K 4096 185 / 69 / 84; 64 experts of 73
   //     rows, K 1024 204 / 126 / 105
+  // M is the buffers' height, and the rows held may be far fewer: 4 of 64 experts with
+  // 64 rows each, N 4096, K 2048 25 us in buffers of 512 rows, 71 in buffers of 4480
+  // (which could take all assignments of 512 tokens).
   const int64_t cus = grid_size();
   if (cus == 0) return MOE_EDEVICE;
   if ((M + 63) / 64 * (K / 64) <= cus) return launch_thin(a, stream);

@@ -5,7 +5,8 @@
 // One pass reads dout once and every expert-output row once and writes every
 // gradient row once, so the kernel is bound by memory: 2 T H + 4 A H bytes for
 // A held assignments (8192 tokens, H 7168, top-8 with the routing gradient: 400
-// us, 5.0 TB/s, what a plain copy reaches).
+// us, 5.0 TB/s, what a plain copy reaches; 4096 tokens, top-16 382 us, 5.1 TB/s, top-32
+// 764 us, 5.0 TB/s: dout is read again for every eight slots, from the caches).
 #include "common.h"
 
 namespace moe {

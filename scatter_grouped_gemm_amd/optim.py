@@ -35,6 +35,8 @@ class AdamW:
     written between steps.  ``master``, ``m``, ``v`` (and ``m_scale``,
     ``v_scale``) are flat over all tensors, tensor i at ``offsets[i]``, a
     multiple of 128; ``v`` holds the codes of its root where state_bits is 8.
+    ``master`` has the places of fp32 parameters too (unused zeros); give them an
+    optimizer of their own where that memory counts.
     ``state_dict`` gives what a checkpoint has to keep (and the fp32 parameters,
     which are the caller's), the seed among it: a run that is taken up again rounds
     as it would have.

@@ -63,6 +63,30 @@ extern "C" {
 /* fp32 tensors of the training calls (weight gradients, parameters). */
 #define MOE_DTYPE_FP32 16
 
+/* Activations of the products with an epilogue (moe_linear, grouped_gemm_*_act)
+ * and of moe_act_bwd.  sigma(x) = 1 / (1 + e^-x), Phi the normal distribution.
+ *   one for each column:
+ *     MOE_ACT_NONE       x
+ *     MOE_ACT_SILU       x sigma(x)
+ *     MOE_ACT_GELU       x Phi(x)
+ *     MOE_ACT_GELU_TANH  x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2
+ *     MOE_ACT_RELU2      max(x, 0)^2
+ *   of the two halves of a row, gate g = columns [0, N/2) and up u = [N/2, N):
+ *     MOE_ACT_SILU_MUL, MOE_ACT_GELU_MUL, MOE_ACT_GELU_TANH_MUL   act(g) u
+ *     MOE_ACT_SWIGLU_CLAMP   g' sigma(alpha g') (u' + 1) with g' = min(g, limit) and
+ *                            u' = u cut to [-limit, limit]; 1e-3 <= alpha <= 1e3,
+ *                            limit > 0 (infinity: not cut).  The others ignore both.
+ * All in fp32.  A NaN stays one; of -infinity, SILU and both GELUs give NaN. */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_SILU 1
+#define MOE_ACT_GELU 2
+#define MOE_ACT_GELU_TANH 3
+#define MOE_ACT_RELU2 4
+#define MOE_ACT_SILU_MUL 9
+#define MOE_ACT_GELU_MUL 10
+#define MOE_ACT_GELU_TANH_MUL 11
+#define MOE_ACT_SWIGLU_CLAMP 12
+
 /* device error word bits (see moe_get_device_error) */
 #define MOE_DEVERR_MASKED_OVERFLOW 1  /* an expert received more than max_m rows */
 
@@ -384,6 +408,65 @@ int32_t moe_combine(const void* Y, int64_t num_rows, const int32_t* src2dst,
                     void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Products with an epilogue.  The product is summed in fp32 over ascending k, and
+ * bias, activation and residual follow in fp32 before the one rounding to the
+ * output's type.  A row's result depends on its own row and its weights alone: it
+ * is the same for any number of rows, and in both layouts.
+ * ------------------------------------------------------------------------- */
+
+/* Dense product: with p[m][n] = sum over k of A[m][k] * B[n][k] + bias[n],
+ *   out[m][:] = act(p[m][:]) + residual[m][:]
+ * (the router's logits; a shared expert, whose second product takes what the
+ * routed experts gave as its residual).
+ *   A            device bf16, row m at A + m*lda (elements)
+ *   B            device bf16 [N][K]
+ *   bias         device bf16 or fp32 [N] (bias_dtype MOE_DTYPE_BF16 or
+ *                MOE_DTYPE_FP32), or NULL
+ *   act, alpha, limit   see MOE_ACT_*; the output has N columns, N/2 with a gated one
+ *   residual     device, of out's type, row m at residual + m*ld_residual, or NULL.
+ *                May be out itself with ld_out, not otherwise overlap it
+ *   out          device, out_dtype MOE_DTYPE_BF16 or MOE_DTYPE_FP32, row m at
+ *                out + m*ld_out
+ *   pre          device bf16 [M][N], out: p for moe_act_bwd, or NULL
+ * Limits: K % 8 == 0, lda % 8 == 0 and >= K, A and B 16-byte aligned, ld_out and
+ * ld_residual at least the output's columns, N even with a gated activation, and then
+ * N * K < 2^30; lda < 2^22, M < 2^31, ceil(M / 128) * ceil(N / 128) < 2^24. */
+int32_t moe_linear(const void* A, int64_t lda, const void* B, const void* bias, int32_t bias_dtype,
+                   int32_t act, float alpha, float limit, const void* residual, int64_t ld_residual,
+                   int32_t out_dtype, void* out, int64_t ld_out, void* pre, int64_t M, int32_t N,
+                   int32_t K, void* stream);
+
+/* grouped_gemm_contig with each expert's bias and an activation: for row r of
+ * expert g = m_indices[r], p[r][:] = A[r, :] . B[g]^T + bias[g][:],
+ *   out[r][:] = act(p[r][:]).
+ *   dtype, A, A_scale, B, B_scale, m_indices   as grouped_gemm_contig
+ *   bias         device bf16 or fp32 [G][N] (bias_dtype), or NULL
+ *   out          out_dtype MOE_DTYPE_BF16: bf16 [M][N], [M][N/2] with a gated
+ *                activation; gated also MOE_DTYPE_FP8_E4M3_UE8M0: e4m3 [M][N/2] with
+ *                out_scale [N/256][M], quantised from the fp32 values
+ *   pre          dtype MOE_DTYPE_BF16 only: device bf16 [M][N], out: p for
+ *                moe_act_bwd, or NULL
+ * Rows with m_indices < 0 are left as they were in every output.
+ * Limits as grouped_gemm_contig; N % 256 == 0 with a gated activation, and then
+ * (N/2 + 256) * K * 2 < 2^32; pointers of tensors 16-byte aligned. */
+int32_t grouped_gemm_contig_act(int32_t dtype, const void* A, const uint8_t* A_scale, const void* B,
+                                const uint8_t* B_scale, const void* bias, int32_t bias_dtype,
+                                int32_t act, float alpha, float limit, int32_t out_dtype, void* out,
+                                uint8_t* out_scale, void* pre, const int32_t* m_indices, int64_t M,
+                                int32_t N, int32_t K, int32_t G, void* stream);
+
+/* The same for the masked layout: rows r < masked_m[g] of group g.
+ *   out [G][max_m][N or N/2]; out_scale [G][N/256][max_m]; pre [G][max_m][N];
+ *   expected_m   as grouped_gemm_masked
+ * Rows at or past masked_m[g] are left as they were in every output. */
+int32_t grouped_gemm_masked_act(int32_t dtype, const void* A, const uint8_t* A_scale, const void* B,
+                                const uint8_t* B_scale, const void* bias, int32_t bias_dtype,
+                                int32_t act, float alpha, float limit, int32_t out_dtype, void* out,
+                                uint8_t* out_scale, void* pre, const int32_t* masked_m,
+                                int32_t expected_m, int32_t max_m, int32_t N, int32_t K, int32_t G,
+                                void* stream);
+
+/* ---------------------------------------------------------------------------
  * Training: gradients of the calls above and the AdamW step.  All BF16 (weights
  * held in FP8 or MX formats have no gradient here).  Device pointers of tensors
  * must be 16-byte aligned -> else MOE_EUNSUPPORTED.  Every gradient is the same
@@ -437,6 +520,37 @@ int32_t moe_scatter_bwd(const void* dX, int64_t num_rows, const int32_t* src2dst
 int32_t silu_and_mul_bwd(const void* gateup, const void* dact, int64_t M, int32_t I,
                          const int32_t* m_indices, const int32_t* masked_m, int32_t max_m,
                          void* dgateup, void* act, void* stream);
+
+/* Scratch bytes moe_act_bwd needs for dbias (G = 1 without a layout): sums of
+ * blocks of rows.  0 on a negative or zero size. */
+size_t moe_act_bwd_ws_bytes(int64_t M, int32_t N, int32_t G);
+
+/* Gradient of the epilogue of moe_linear and grouped_gemm_*_act (the residual's
+ * gradient is dout itself).  With p = pre[r],
+ *   dpre[r][:] = dout[r][:] * act'(p)          rounded once to bf16
+ *   dbias[g][n] = sum over g's rows of dpre[r][n] as it was before that rounding
+ *                 (fp32), added to what dbias holds if accumulate is not 0, and
+ *                 rounded once to its type
+ * At a gate or up part that equals its limit the cut passes the gradient on, past
+ * it the part's gradient is 0.
+ *   Rows: m_indices (compact), masked_m with max_m (masked; M = G*max_m) or, both
+ *   NULL, every row (then G = 1).  Other rows of dpre are left as they were and are
+ *   part of no sum.
+ *   pre, dpre    bf16 [M][N]; dpre may be pre, and may be dout where the activation
+ *                is not gated.  With MOE_ACT_NONE pre is not read, and dpre may be
+ *                NULL: the bias gradient alone
+ *   dout         bf16 [M][N], [M][N/2] with a gated activation
+ *   expert_start_loc, num_valid   device int32 [G], needed with m_indices and dbias
+ *   dbias        dbias_dtype MOE_DTYPE_BF16 or MOE_DTYPE_FP32 [G][N], or NULL.  An
+ *                expert without rows gets 0 (or keeps what it holds)
+ *   ws, ws_bytes scratch for dbias, at least moe_act_bwd_ws_bytes(M, N, G)
+ * Limits: N % 8 == 0 (16 with a gated activation), N <= 2^27, M < 2^26, G <= 65535;
+ * pointers of tensors 16-byte aligned. */
+int32_t moe_act_bwd(const void* pre, const void* dout, int64_t M, int32_t N, int32_t act,
+                    float alpha, float limit, const int32_t* m_indices, const int32_t* masked_m,
+                    int32_t max_m, const int32_t* expert_start_loc, const int32_t* num_valid,
+                    int32_t G, void* dpre, int32_t dbias_dtype, int32_t accumulate, void* dbias,
+                    void* ws, size_t ws_bytes, void* stream);
 
 /* Gradient of grouped_gemm_contig with respect to A:
  *   dA[r][:] = dC[r][:] . B[m_indices[r]]   (the sum runs over N, in fp32)

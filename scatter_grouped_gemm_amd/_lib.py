@@ -20,11 +20,16 @@ MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_ECAPACITY, MOE_EDEVICE = 0, 1, 2, 3, 4
 MOE_DTYPE_BF16, MOE_DTYPE_FP8_E4M3_UE8M0, MOE_DTYPE_FP8_E4M3_MXFP8, MOE_DTYPE_FP8_MXFP4 = 0, 1, 2, 3
 MOE_DTYPE_FP32 = 16
 MOE_MX_E4M3, MOE_MX_E2M1 = 0, 1
+# activations of the products with an epilogue; the gated ones take two halves of a row
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu2": 4,
+               "silu_mul": 9, "gelu_mul": 10, "gelu_tanh_mul": 11, "swiglu_clamp": 12}
+GATED_ACTIVATIONS = ("silu_mul", "gelu_mul", "gelu_tanh_mul", "swiglu_clamp")
 MOE_DEVERR_MASKED_OVERFLOW = 1
 MOE_SCATTER_NOALLOC_MAX_BYTES = 4 << 20
 
 # name -> (restype, argtypes); the exported symbols of include/moe.h
 _P, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+_F = ctypes.c_float
 SIGNATURES = {
     "moe_compact_rows_bound": (_I64, [_I64, _I32, _I32]),
     "moe_use_masked_layout": (_I32, [_I32, _I32]),
@@ -59,6 +64,13 @@ SIGNATURES = {
     "silu_and_mul_bwd": (_I32, [_P, _P, _I64, _I32, _P, _P, _I32, _P, _P, _P]),
     "grouped_gemm_contig_dgrad": (_I32, [_P, _P, _P, _P, _I64, _I32, _I32, _I32, _P]),
     "grouped_gemm_contig_wgrad": (_I32, [_P, _P, _P, _P, _I32, _I32, _P, _I64, _I32, _I32, _I32, _P]),
+    "moe_linear": (_I32, [_P, _I64, _P, _P, _I32, _I32, _F, _F, _P, _I64, _I32, _P, _I64, _P, _I64, _I32, _I32, _P]),
+    "grouped_gemm_contig_act": (_I32, [_I32, _P, _P, _P, _P, _P, _I32, _I32, _F, _F, _I32, _P, _P, _P, _P, _I64,
+                                       _I32, _I32, _I32, _P]),
+    "grouped_gemm_masked_act": (_I32, [_I32, _P, _P, _P, _P, _P, _I32, _I32, _F, _F, _I32, _P, _P, _P, _P, _I32,
+                                       _I32, _I32, _I32, _I32, _P]),
+    "moe_act_bwd_ws_bytes": (_SZ, [_I64, _I32, _I32]),
+    "moe_act_bwd": (_I32, [_P, _P, _I64, _I32, _I32, _F, _F, _P, _P, _I32, _P, _P, _I32, _P, _I32, _I32, _P, _P, _SZ, _P]),
     "moe_adamw_plan_bytes": (_SZ, [_P, _I32]),
     "moe_adamw_plan": (_I32, [_P, _I32, _P, _SZ]),
     "moe_adamw_step": (_I32, [_P, _SZ, _P, _P, _P, ctypes.c_double, ctypes.c_double, ctypes.c_float,
@@ -420,6 +432,161 @@ def silu_and_mul_bwd(gateup, dact, dgateup, act=None, m_indices=None, masked_m=N
         None if masked_m is None else _dev("masked_m", _INT32, masked_m.shape, masked_m, dev), max_m,
         _dev("dgateup", _BF16, (M, N), dgateup, dev),
         None if act is None else _dev("act", _BF16, (M, I), act, dev), _raw_stream(dev)))
+
+
+def _act(act: str) -> int:
+    try:
+        return ACTIVATIONS[act]
+    except KeyError:
+        raise ValueError(f"unknown activation {act!r}: one of {', '.join(ACTIVATIONS)}") from None
+
+
+def _rows(name: str, dtype, shape, t, dev: int):
+    """Data pointer and row stride of a matrix on the current device whose rows are contiguous."""
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name}: want {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: is on {t.device}, not on the current device")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _bias(bias, shape, dev: int):
+    """Pointer and type of a bias, or (None, 0)."""
+    if bias is None:
+        return None, MOE_DTYPE_BF16
+    if bias.dtype is _F32:
+        return _dev("bias", _F32, shape, bias, dev), MOE_DTYPE_FP32
+    return _dev("bias", _BF16, shape, bias, dev), MOE_DTYPE_BF16
+
+
+def moe_linear(x, w, out, bias=None, act="none", residual=None, pre=None, alpha=1.702, limit=7.0):
+    """out = act(x w^T + bias) + residual: x bf16 [T, K], w bf16 [N, K], out bf16 or
+    fp32 [T, N] ([T, N/2] with a gated activation).  Rows of x, out and residual
+    (out's type; may be out) may be a stride apart.  pre bf16 [T, N] receives the
+    product with its bias, which moe_act_bwd needs."""
+    _need(x.dim() == 2 and w.dim() == 2, "moe_linear: x is [T, K] and w [N, K]")
+    code = _act(act)
+    T, K = x.shape
+    N = w.shape[0]
+    _need(code < 8 or N % 2 == 0, "moe_linear: a gated activation takes an even number of columns")
+    _need(out.dtype in (_BF16, _F32), "moe_linear: out is bf16 or fp32")
+    dev = _current()
+    shape = (T, N // 2 if code >= 8 else N)
+    px, ldx = _rows("x", _BF16, (T, K), x, dev)
+    po, ldo = _rows("out", out.dtype, shape, out, dev)
+    pr, ldr = (None, 0) if residual is None else _rows("residual", out.dtype, shape, residual, dev)
+    pb, bdt = _bias(bias, (N,), dev)
+    _check("moe_linear", lib().moe_linear(
+        px, ldx, _dev("w", _BF16, (N, K), w, dev), pb, bdt, code, alpha, limit, pr, ldr,
+        MOE_DTYPE_FP32 if out.dtype is _F32 else MOE_DTYPE_BF16, po, ldo,
+        None if pre is None else _dev("pre", _BF16, (T, N), pre, dev), T, N, K, _raw_stream(dev)))
+
+
+def _product_operands(name, fp8, A, A_scale, B, B_scale, out, out_scale, rows, K, G, N, K2, cols, per_row, dev):
+    """Pointers of a grouped product's tensors: (A, A_scale, B, B_scale, out dtype, out, out_scale)."""
+    adt = torch.uint8 if fp8 else _BF16
+    q8 = out.dtype is torch.uint8
+    _need(K == K2, f"{name}: A and B differ in their reduction")
+    _need(q8 or out.dtype is _BF16, f"{name}: out is bf16 or uint8 (e4m3)")
+    u8 = lambda what, t, n: _scale(what, t, n, dev)  # noqa: E731
+    n_scale = rows * (K // 128)
+    w_scale = 0 if not fp8 else G * N * (K // 32) if fp8 in ("mxfp8", "mxfp4") else G * (N // 128) * (K // 128)
+    return (_dev("A", adt, A.shape, A, dev), u8("A_scale", A_scale, n_scale) if fp8 else None,
+            _dev("B", adt, B.shape, B, dev), u8("B_scale", B_scale, w_scale) if fp8 else None,
+            MOE_DTYPE_FP8_E4M3_UE8M0 if q8 else MOE_DTYPE_BF16, _dev("out", out.dtype, per_row + (cols,), out, dev),
+            u8("out_scale", out_scale, rows * (cols // 128)) if q8 else None)
+
+
+def _scale(name: str, t, n: int, dev: int):
+    _need(t is not None, f"{name}: needed with FP8")
+    _need(t.numel() == n, f"{name}: want {n} bytes, got {t.numel()}")
+    return _dev(name, torch.uint8, t.shape, t, dev)
+
+
+def grouped_gemm_contig_act(fp8, A, A_scale, B, B_scale, out, m_indices, bias=None, act="none", out_scale=None,
+                            pre=None, alpha=1.702, limit=7.0):
+    """Compact-layout product with each expert's bias [G, N] and an activation: out
+    [M, N], [M, N/2] with a gated one (then also e4m3 with out_scale [N/256, M]).
+    pre [M, N] (bf16 weights) receives the product with its bias for moe_act_bwd.
+    Rows with m_indices < 0 keep what they hold."""
+    _need(A.dim() == 2 and B.dim() == 3, "grouped_gemm_contig_act: A is [M, K] and B [G, N, K]")
+    code = _act(act)
+    M, K = A.shape
+    G, N, K2 = _bk(fp8, B)
+    dev = _current()
+    ops = _product_operands("grouped_gemm_contig_act", fp8, A, A_scale, B, B_scale, out, out_scale, M, K, G, N, K2,
+                            N // 2 if code >= 8 else N, (M,), dev)
+    pb, bdt = _bias(bias, (G, N), dev)
+    _check("grouped_gemm_contig_act", lib().grouped_gemm_contig_act(
+        _gemm_dtype(fp8), *ops[:4], pb, bdt, code, alpha, limit, *ops[4:],
+        None if pre is None else _dev("pre", _BF16, (M, N), pre, dev), _dev("m_indices", _INT32, (M,), m_indices, dev),
+        M, N, K, G, _raw_stream(dev)))
+
+
+def grouped_gemm_masked_act(fp8, A, A_scale, B, B_scale, out, masked_m, expected_m, bias=None, act="none",
+                            out_scale=None, pre=None, alpha=1.702, limit=7.0):
+    """grouped_gemm_contig_act for the masked layout: out [G, max_m, N or N/2], FP8
+    out_scale [G, N/256, max_m], pre [G, max_m, N].  Rows at or past masked_m keep
+    what they hold."""
+    _need(A.dim() == 3 and B.dim() == 3, "grouped_gemm_masked_act: A is [G, max_m, K] and B [G, N, K]")
+    code = _act(act)
+    G2, max_m, K = A.shape
+    G, N, K2 = _bk(fp8, B)
+    _need(G == G2, "grouped_gemm_masked_act: A and B differ in their experts")
+    dev = _current()
+    ops = _product_operands("grouped_gemm_masked_act", fp8, A, A_scale, B, B_scale, out, out_scale, G * max_m, K, G, N,
+                            K2, N // 2 if code >= 8 else N, (G, max_m), dev)
+    pb, bdt = _bias(bias, (G, N), dev)
+    _check("grouped_gemm_masked_act", lib().grouped_gemm_masked_act(
+        _gemm_dtype(fp8), *ops[:4], pb, bdt, code, alpha, limit, *ops[4:],
+        None if pre is None else _dev("pre", _BF16, (G, max_m, N), pre, dev), _dev("masked_m", _INT32, (G,), masked_m, dev),
+        expected_m, max_m, N, K, G, _raw_stream(dev)))
+
+
+def moe_act_bwd_ws_bytes(M: int, N: int, G: int) -> int:
+    return int(lib().moe_act_bwd_ws_bytes(M, N, G))
+
+
+def moe_act_bwd(pre, dout, dpre, act, dbias=None, m_indices=None, expert_start_loc=None, num_valid=None, masked_m=None,
+                max_m=0, alpha=1.702, limit=7.0, accumulate=False, ws=None):
+    """Gradient of the epilogue of moe_linear and the grouped products: dpre [M, N]
+    (may be pre) from pre [M, N] and dout [M, N or N/2], and the bias gradients
+    dbias [G, N] ([N] or [1, N] without a layout) in bf16 or fp32, replaced or
+    (accumulate) added to.  Rows: m_indices (with expert_start_loc and num_valid for
+    dbias), masked_m with max_m, or all.  act "none": pre and dpre may be None.  ws:
+    scratch of moe_act_bwd_ws_bytes, allocated here if not given."""
+    code = _act(act)
+    _need(dout.dim() == 2, "moe_act_bwd: dout is a matrix")
+    M, cols = dout.shape
+    N = 2 * cols if code >= 8 else cols
+    _need(code == 0 or (pre is not None and dpre is not None), "moe_act_bwd: pre and dpre are needed")
+    _need(masked_m is None or (max_m > 0 and masked_m.numel() * max_m == M),
+          "moe_act_bwd: masked_m and max_m do not make up M rows")
+    dev = _current()
+    G, pd, pw, nw, ddt, pst, pnv = 1, None, None, 0, MOE_DTYPE_FP32, None, None
+    if dbias is not None:
+        if masked_m is not None:
+            G = masked_m.numel()
+        elif m_indices is not None:
+            _need(expert_start_loc is not None and num_valid is not None,
+                  "moe_act_bwd: dbias in the compact layout needs expert_start_loc and num_valid")
+            G = num_valid.numel()
+            pst = _dev("expert_start_loc", _INT32, (G,), expert_start_loc, dev)
+            pnv = _dev("num_valid", _INT32, (G,), num_valid, dev)
+        _need(dbias.dtype in (_BF16, _F32), "moe_act_bwd: dbias is bf16 or fp32")
+        ddt = MOE_DTYPE_FP32 if dbias.dtype is _F32 else MOE_DTYPE_BF16
+        pd = _dev("dbias", dbias.dtype, (N,) if dbias.dim() == 1 and G == 1 else (G, N), dbias, dev)
+        if ws is None:
+            ws = torch.empty(moe_act_bwd_ws_bytes(M, N, G), dtype=torch.uint8, device=dout.device)
+        pw, nw = _dev("ws", ws.dtype, ws.shape, ws, dev), ws.numel() * ws.element_size()
+    _check("moe_act_bwd", lib().moe_act_bwd(
+        None if pre is None else _dev("pre", _BF16, (M, N), pre, dev), _dev("dout", _BF16, (M, cols), dout, dev), M, N, code,
+        alpha, limit, None if m_indices is None else _dev("m_indices", _INT32, (M,), m_indices, dev),
+        None if masked_m is None else _dev("masked_m", _INT32, masked_m.shape, masked_m, dev), max_m, pst, pnv, G,
+        None if dpre is None else _dev("dpre", _BF16, (M, N), dpre, dev), ddt, int(bool(accumulate)), pd, pw, nw,
+        _raw_stream(dev)))
 
 
 def grouped_gemm_contig_dgrad(dC, B, dA, m_indices):

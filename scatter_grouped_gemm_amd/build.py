@@ -17,9 +17,9 @@ LIB = os.path.join(PKG, "libmoe.so")
 OBJDIR = os.path.join(PKG, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-SOURCES = ["route.hip", "scatter.hip", "quant.hip", "combine.hip", "gemm.hip", "gemm_wreg.hip",
+SOURCES = ["route.hip", "scatter.hip", "quant.hip", "combine.hip", "gemm.hip", "gemm_act.hip", "gemm_wreg.hip",
            "token_grad.hip", "silu_bwd.hip", "gemm_grad.hip", "dgrad_short.hip", "wgrad_short.hip",
-           "adamw.hip"]
+           "adamw.hip", "linear.hip", "act_bwd.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",

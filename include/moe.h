@@ -430,7 +430,7 @@ int32_t moe_combine(const void* Y, int64_t num_rows, const int32_t* src2dst,
  *   pre          device bf16 [M][N], out: p for moe_act_bwd, or NULL
  * Limits: K % 8 == 0, lda % 8 == 0 and >= K, A and B 16-byte aligned, ld_out and
  * ld_residual at least the output's columns, N even with a gated activation, and then
- * N * K < 2^30; lda < 2^22, M < 2^31, ceil(M / 128) * ceil(N / 128) < 2^24. */
+ * (N/2 + 256) * K * 2 < 2^32; lda < 2^22, M < 2^31, ceil(M / 128) * ceil(N / 128) < 2^24. */
 int32_t moe_linear(const void* A, int64_t lda, const void* B, const void* bias, int32_t bias_dtype,
                    int32_t act, float alpha, float limit, const void* residual, int64_t ld_residual,
                    int32_t out_dtype, void* out, int64_t ld_out, void* pre, int64_t M, int32_t N,

@@ -1,6 +1,7 @@
 // Entry points of the grouped products with a bias and an activation in their
 // epilogue (gemm_kernel.h: kEpiBias, kEpiAct*).
 #include "gemm_kernel.h"
+#include "linear.h"
 
 namespace moe {
 namespace {
@@ -58,8 +59,29 @@ extern "C" int32_t grouped_gemm_contig_act(int32_t dtype, const void* A, const u
   const int32_t st = act_args(dtype, A, A_scale, B, B_scale, bias, bias_dtype, act, alpha, limit, out_dtype, out,
                               out_scale, pre, m_indices, M, N, K, G, a);
   if (st != MOE_OK || M == 0) return st;
+  if ((M + 127) / 128 > 8176) return MOE_EUNSUPPORTED;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (out_dtype == MOE_DTYPE_FP8_E4M3_UE8M0) return launch_dtype<128, 256, false, kEpiActFp8>(dtype, a, s);
+  if (dtype == MOE_DTYPE_BF16) {
+    LinearArgs l{};
+    l.A = a.A;
+    l.lda = static_cast<int64_t>(K) * 2;
+    l.B = a.B;
+    l.bias = bias;
+    l.bias32 = a.bias32;
+    l.out = out;
+    l.cols = a.act.gated ? N / 2 : N;
+    l.ldo = l.cols;
+    l.pre = a.pre;
+    l.m_indices = m_indices;
+    l.M = M;
+    l.N = N;
+    l.K = K;
+    l.G = G;
+    l.act = a.act;
+    linear_alignment(l);
+    return launch_linear(l, s);
+  }
   if (a.act.gated) return launch_dtype<128, 256, false, kEpiActBf16>(dtype, a, s);
   if (N % 256 == 0) return launch_dtype<128, 256, false, kEpiBias>(dtype, a, s);
   return launch_dtype<128, 128, false, kEpiBias>(dtype, a, s);

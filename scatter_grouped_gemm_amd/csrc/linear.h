@@ -19,10 +19,19 @@ struct LinearArgs {
   int N, K, G, cols;       // cols: of the output
   int bias32, out32;
   int vec;                 // groups of four columns are whole and aligned in every tensor of the epilogue
+  int vec8;                // groups of eight are, in the tensors of 16-bit values
   ActArgs act;
 };
 
-int32_t launch_linear_tile(const LinearArgs& a, hipStream_t stream);
+// The kernel that the sizes ask for; arguments are checked by the caller.
+int32_t launch_linear(const LinearArgs& a, hipStream_t stream);
+
+// linear_wide.hip: whether it covers the call, and the launch.
+bool linear_wide_covers(const LinearArgs& a);
+int32_t launch_linear_wide(const LinearArgs& a, hipStream_t stream);
+
+// Sets vec and vec8 from the other fields.
+void linear_alignment(LinearArgs& a);
 
 namespace {
 
@@ -33,6 +42,11 @@ typedef __attribute__((ext_vector_type(4))) float lin_f4;
 __device__ __forceinline__ lin_f4 unpack_bf16x4(lin_u32x2 b) {
   return lin_f4{__uint_as_float(b[0] << 16), __uint_as_float(b[0] & 0xffff0000u),
                 __uint_as_float(b[1] << 16), __uint_as_float(b[1] & 0xffff0000u)};
+}
+
+// A descriptor of up to 2^32 - 1 bytes: reads behind them give zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_u(const uint8_t* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, static_cast<int>(bytes), 0x00020000);
 }
 
 // Four values from element `at` of an array of fp32 or bf16; of the columns n .. n + 3

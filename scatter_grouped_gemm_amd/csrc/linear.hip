@@ -18,7 +18,7 @@
 namespace moe {
 namespace {
 
-constexpr uint32_t kOutside = 0x7ffffff0u;  // beyond any descriptor here
+constexpr uint32_t kOutside = 0xfffffff0u;  // beyond any descriptor here
 
 template <int BM, int BN, bool GATED>
 __global__ __launch_bounds__(256, 2) void linear_tile_kernel(const LinearArgs a) {
@@ -34,10 +34,18 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(const LinearArgs a)
   const int nct = (a.cols + NC - 1) / NC;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x / nct) * BM;
   const int col0 = static_cast<int>(blockIdx.x % nct) * NC;
-  const int rows = a.M - row0 < BM ? static_cast<int>(a.M - row0) : BM;
+  int e = 0, rows = a.M - row0 < BM ? static_cast<int>(a.M - row0) : BM;
+  if (a.m_indices) {  // a block of 128 rows has one expert, and its valid rows come first
+    e = __builtin_amdgcn_readfirstlane(a.m_indices[row0]);
+    if (e < 0 || e >= a.G) return;
+    int valid = 0;
+#pragma unroll
+    for (int h = 0; h < BM; h += 64) valid += static_cast<int>(__popcll(__ballot(h + lane < rows && a.m_indices[row0 + h + lane] >= 0)));
+    rows = valid;
+  }
   const int64_t ldb = static_cast<int64_t>(a.K) * 2;
 
-  // Offsets of this lane's 16 bytes from the tile's first row of A and of B (below 2^31
+  // Offsets of this lane's 16 bytes from the tile's first row of A and of B (below 2^32
   // by the limits of the call).
   uint32_t va[LA], vb[LB];
   const int chunk = (lane & 7) ^ (lane >> 3);  // of the row's 128 bytes: a load covers 8 rows
@@ -62,17 +70,18 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(const LinearArgs a)
     vb[j] = in ? static_cast<uint32_t>(n * ldb) + chunk * 16 : kOutside;
   }
   const uint8_t* pa = a.A + row0 * a.lda;
-  const uint8_t* pb = a.B + col0 * ldb;
+  const uint8_t* pb = a.B + (static_cast<int64_t>(e) * a.N + col0) * ldb;
   const int na = rows * static_cast<int>(a.lda);       // bytes of the tile's rows
-  const int nrb = GATED || a.N - col0 < BN ? a.N - col0 : BN;
-  const int nb = static_cast<int>(nrb * ldb);          // gated: up to B's end
+  int nr = GATED ? a.cols + NC : BN;                    // B rows that the tile's offsets reach
+  nr = nr < a.N - col0 ? nr : a.N - col0;
+  const uint32_t nb = static_cast<uint32_t>(nr * ldb);
   const int steps = (a.K + kStep - 1) / kStep;
   int loaded = 0;
   auto load = [&](uint8_t* s) __attribute__((always_inline)) {
     // behind the last step nothing is read, but the same number of loads is issued
     const int left = a.K - loaded * kStep;
     const bool in = chunk * 8 < left;
-    const auto ra = buffer(pa, left > 0 ? na - loaded * (kStep * 2) : 0), rb = buffer(pb, left > 0 ? nb - loaded * (kStep * 2) : 0);
+    const auto ra = buffer(pa, left > 0 ? na - loaded * (kStep * 2) : 0), rb = buffer_u(pb, left > 0 ? nb - loaded * (kStep * 2) : 0);
 #pragma unroll
     for (int j = 0; j < LA; ++j)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (__attribute__((address_space(3))) void*)(s + (wave * LA + j) * 1024), 16,
@@ -130,14 +139,14 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(const LinearArgs a)
 #pragma unroll
   for (int j = 0; j < TH; ++j) {
     const int n = cw + j * 16;
-    const f32x4 bg = bias4(a, 0, n, a.cols);
+    const f32x4 bg = bias4(a, e, n, a.cols);
     f32x4 bu{};
     if constexpr (GATED)
-      if (a.bias) bu = load4(a.bias, a.bias32, a.vec, a.cols + n, n, a.cols);
+      if (a.bias) bu = load4(a.bias, a.bias32, a.vec, static_cast<int64_t>(e) * a.N + a.cols + n, n, a.cols);
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-      const int64_t r = row0 + wm * WM + i * 16 + fr;
-      if (r < a.M) finish4<GATED>(a, r, n, acc[j][i] + bg, GATED ? acc[(j + TH) % TN][i] + bu : bg);
+      const int r = wm * WM + i * 16 + fr;
+      if (r < rows) finish4<GATED>(a, row0 + r, n, acc[j][i] + bg, GATED ? acc[(j + TH) % TN][i] + bu : bg);
     }
   }
 #endif
@@ -160,10 +169,20 @@ inline bool aligned(const void* p, int bytes) { return (reinterpret_cast<uintptr
 
 }  // namespace
 
-int32_t launch_linear_tile(const LinearArgs& a, hipStream_t s) {
+void linear_alignment(LinearArgs& a) {
+  const int os = a.out32 ? 4 : 2;
+  a.vec = a.cols % 4 == 0 && a.ldo % 4 == 0 && aligned(a.out, 4 * os) &&
+          (!a.residual || (a.ldr % 4 == 0 && aligned(a.residual, 4 * os))) && (!a.pre || aligned(a.pre, 8)) &&
+          (!a.bias || aligned(a.bias, a.bias32 ? 16 : 8));
+  a.vec8 = a.vec && a.cols % 8 == 0 && a.ldo % 8 == 0 && aligned(a.out, 16) &&
+           (!a.residual || (a.ldr % 8 == 0 && aligned(a.residual, 16))) && (!a.pre || aligned(a.pre, 16));
+}
+
+int32_t launch_linear(const LinearArgs& a, hipStream_t s) {
+  const int64_t n = a.N;
+  if (linear_wide_covers(a) && (a.M + 255) / 256 * ((n + 255) / 256) >= 200) return launch_linear_wide(a, s);
   // tiles of 128 x 128 where they fill the card
-  const int64_t big = (a.M + 127) / 128 * ((a.N + 127) / 128);
-  return big >= 256 ? launch<128, 128>(a, s) : launch<64, 64>(a, s);
+  return (a.M + 127) / 128 * ((n + 127) / 128) >= 256 ? launch<128, 128>(a, s) : launch<64, 64>(a, s);
 }
 
 }  // namespace moe
@@ -183,8 +202,8 @@ extern "C" int32_t moe_linear(const void* A, int64_t lda, const void* B, const v
   if (out_dtype != MOE_DTYPE_BF16 && out_dtype != MOE_DTYPE_FP32) return MOE_EUNSUPPORTED;
   if (bias && bias_dtype != MOE_DTYPE_BF16 && bias_dtype != MOE_DTYPE_FP32) return MOE_EUNSUPPORTED;
   if (K % 8 != 0 || lda % 8 != 0) return MOE_EUNSUPPORTED;
-  // offsets within a tile's rows are 31-bit; a gated tile's reach B's last row
-  if (lda >= (1 << 22) || (a.act.gated && static_cast<int64_t>(N) * K >= (1 << 30))) return MOE_EUNSUPPORTED;
+  // offsets within a tile's rows are 32-bit; a gated tile's reach the up rows
+  if (lda >= (1 << 22) || (a.act.gated && (static_cast<int64_t>(N) / 2 + 256) * K * 2 >= (1ll << 32))) return MOE_EUNSUPPORTED;
   if (M >= (1ll << 31) || (M + 127) / 128 * ((static_cast<int64_t>(N) + 127) / 128) >= (1 << 24)) return MOE_EUNSUPPORTED;
   if (M == 0) return MOE_OK;
   if (!A || !B || !out) return MOE_EINVAL;
@@ -207,8 +226,6 @@ extern "C" int32_t moe_linear(const void* A, int64_t lda, const void* B, const v
   a.N = N;
   a.K = K;
   a.G = 1;
-  a.vec = a.cols % 4 == 0 && ld_out % 4 == 0 && aligned(out, 4 * os) &&
-          (!residual || (ld_residual % 4 == 0 && aligned(residual, 4 * os))) && (!pre || aligned(pre, 8)) &&
-          (!bias || aligned(bias, a.bias32 ? 16 : 8));
-  return launch_linear_tile(a, static_cast<hipStream_t>(stream));
+  linear_alignment(a);
+  return launch_linear(a, static_cast<hipStream_t>(stream));
 }

@@ -28,7 +28,7 @@ def linear(A=P, lda=256, B=P, bias=None, bdt=0, act=0, alpha=1.702, limit=7.0, r
     (dict(A=BAD), L.MOE_EUNSUPPORTED), (dict(B=BAD), L.MOE_EUNSUPPORTED), (dict(out=4097), L.MOE_EUNSUPPORTED),
     (dict(odt=16, out=4098), L.MOE_EUNSUPPORTED), (dict(bias=4098, bdt=16), L.MOE_EUNSUPPORTED),
     (dict(pre=4097), L.MOE_EUNSUPPORTED), (dict(lda=1 << 22), L.MOE_EUNSUPPORTED),
-    (dict(act=9, N=1 << 20, K=1024, lda=1024, ldo=1 << 20), L.MOE_EUNSUPPORTED),
+    (dict(act=9, N=1 << 20, K=4096, lda=4096, ldo=1 << 20), L.MOE_EUNSUPPORTED),
     (dict(M=(1 << 30), N=1 << 20, ldo=1 << 20), L.MOE_EUNSUPPORTED),
     (dict(M=0, A=None, B=None, out=None), L.MOE_OK),
 ])

@@ -79,6 +79,7 @@ extern "C" int32_t grouped_gemm_contig_act(int32_t dtype, const void* A, const u
     l.K = K;
     l.G = G;
     l.act = a.act;
+    l.deep = M >= 1024ll * G;
     linear_alignment(l);
     return launch_linear(l, s);
   }

@@ -110,9 +110,9 @@ struct Tile {
 // Position pos of the order -> tile (rows <= 0: an empty position).  Run-table
 // entries (P = first position, first row, valid rows, expert) are sorted by P;
 // the cursor only moves forward since a workgroup's positions increase.  Tile
-// heights are rounded up to a multiple of Q rows.
+// heights are rounded up to a multiple of Q rows (or of another power of two).
 template <int Q>
-__device__ __forceinline__ Tile decode(const int4* table, int nr, int& cur, int pos, int ntn) {
+__device__ __forceinline__ Tile decode(const int4* table, int nr, int& cur, int pos, int ntn, int quantum = Q) {
   int4 r;
   int nt;
   for (;;) {
@@ -133,7 +133,7 @@ __device__ __forceinline__ Tile decode(const int4* table, int nr, int& cur, int 
   const int rest = q - mg * kGM * ntn;
   const int ntile = gsz > 0 ? rest / gsz : 0;
   const int m = m0 + rest - ntile * gsz;
-  const int h = ((r.z + nt - 1) / nt + Q - 1) / Q * Q;
+  const int h = ((r.z + nt - 1) / nt + quantum - 1) / quantum * quantum;
   const int r0 = m * h;
   t.rows = (q < 0 || q >= nt * ntn || gsz <= 0) ? 0 : min(h, r.z - r0);
   t.row = static_cast<int64_t>(r.y) + r0;
@@ -151,7 +151,7 @@ struct Share {
 // Builds the run table of this workgroup's XCD share into `table` (kTable
 // entries of LDS), using three pieces of LDS (free afterwards): the first-row
 // ids and the valid rows of the run ending at each 128-row block (kMaxBlocks
-// ints each) and 2 * WAVES ints for the scans.  All 64 * WAVES threads call it;
+// ints each) and 2 * WAVES ints for the scans (COST: two more).  All 64 * WAVES threads call it;
 // it ends with a barrier.  Returns false when the workgroup has no position to
 // run.
 // FULL: the rows of a run are all valid (a block whose last row is not ends it);
@@ -160,11 +160,20 @@ struct Share {
 // N and K 256 216 us, 209 without; up to 600 blocks no difference.
 // Every run has a tile, and a share no more tiles than an eighth of the blocks
 // and two, so kTable entries hold the runs of either kind.
+// COST: the shares are equal in time and not in positions, where a run's tiles are 256
+// rows and a last one of up to 128 rows costs 9/16 of the others (by_cost false: all the
+// same).
+constexpr int kWhole = 16, kHalf = 9;
+__device__ __forceinline__ int cost_of(int z, bool by_cost) {
+  const int more = tiles_of(z) - 1;
+  return more * kWhole + (by_cost && z - more * kTileRows <= kTileRows / 2 ? kHalf : kWhole);
+}
 constexpr int kPartial = 1 << 16;  // in ids: the block is not full (ids are below 1024 then)
 static_assert(kMaxBlocks / 8 + 2 <= kTable, "the run table holds a share of single blocks");
-template <int WAVES, bool FULL = false>
+template <int WAVES, bool FULL = false, bool COST = false>
 __device__ __forceinline__ bool build_share(const int32_t* __restrict__ m_indices, int64_t M, int G,
-                                            int ntn, int* ids, int* zv, int* scr, int4* table, Share& sh) {
+                                            int ntn, int* ids, int* zv, int* scr, int4* table, Share& sh,
+                                            bool by_cost = false) {
   constexpr int kThreads = 64 * WAVES;
   const int tid = threadIdx.x;
   const int nblk = static_cast<int>((M + 127) / 128);
@@ -195,6 +204,7 @@ __device__ __forceinline__ bool build_share(const int32_t* __restrict__ m_indice
   // valid rows come first, so a binary search for its first negative entry)
   // and M-tiles
   int cnt = 0, tsum = 0;
+  [[maybe_unused]] int csum = 0;
   {
     int S = carry;
     for (int j = j0; j < j1; ++j) {
@@ -212,6 +222,7 @@ __device__ __forceinline__ bool build_share(const int32_t* __restrict__ m_indice
         zv[j] = z;
         ++cnt;
         tsum += tiles_of(z);
+        if constexpr (COST) csum += cost_of(z, by_cost);
       }
     }
   }
@@ -220,8 +231,34 @@ __device__ __forceinline__ bool build_share(const int32_t* __restrict__ m_indice
   const int U = tot.y * ntn;  // positions of the whole order
   const int per_xcd = gridDim.x >> 3;
   const int xcd = blockIdx.x & 7;
-  const int lo_x = static_cast<int>((static_cast<int64_t>(U) * xcd) >> 3);
-  const int hi_x = static_cast<int>((static_cast<int64_t>(U) * (xcd + 1)) >> 3);
+  int lo_x = static_cast<int>((static_cast<int64_t>(U) * xcd) >> 3);
+  int hi_x = static_cast<int>((static_cast<int64_t>(U) * (xcd + 1)) >> 3);
+  if constexpr (COST) {
+    // the positions at which xcd / 8 and (xcd + 1) / 8 of the cost are reached, as if the
+    // cost were spread evenly over a run's positions
+    int2 ctot;
+    const int2 cb0 = scan_excl_sum2<WAVES>(csum, 0, scr, ctot);
+    int* const cut = scr + 2 * WAVES;
+    if (tid < 2) cut[tid] = U;
+    __syncthreads();
+    int mb = base.y, cb = cb0.x;
+    for (int j = j0; j < j1; ++j) {
+      const int v = id(j);
+      if (v >= 0 && (j == nblk - 1 || id(j + 1) != ids[j])) {
+        const int nt = tiles_of(zv[j]), c = cost_of(zv[j], by_cost);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int64_t at = ((static_cast<int64_t>(ctot.x) * (xcd + e) * ntn) >> 3) - static_cast<int64_t>(cb) * ntn;
+          if (at >= 0 && at < static_cast<int64_t>(c) * ntn) cut[e] = mb * ntn + static_cast<int>(at * nt / c);
+        }
+        mb += nt;
+        cb += c;
+      }
+    }
+    __syncthreads();
+    lo_x = cut[0];
+    hi_x = cut[1];
+  }
   // runs ending at or before lo_x, runs starting before hi_x
   int c_lo = 0, c_hi = 0;
   {

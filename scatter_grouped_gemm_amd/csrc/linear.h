@@ -19,6 +19,7 @@ struct LinearArgs {
   int N, K, G, cols;       // cols: of the output
   int bias32, out32;
   int vec;                 // groups of four columns are whole and aligned in every tensor of the epilogue
+  int deep;                // compact layout: many rows an expert (linear_wide.hip)
   int vec8;                // groups of eight are, in the tensors of 16-bit values
   ActArgs act;
 };

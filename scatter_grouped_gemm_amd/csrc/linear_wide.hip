@@ -15,6 +15,14 @@
 //   - The loop is one stream of steps over all of a workgroup's tiles: the loads cross
 //     into the next tile while the current one is finished.  Tiles in the order of
 //     gemm_runs.h; one matrix is one run.
+//   - A tile of up to 128 rows leaves out the MFMAs and reads of its lower half.  An
+//     expert's rows are cut 256 at a time where they are many (deep: 1024 an expert, by
+//     the buffers' height), and the XCDs' shares made equal with the last tile counted
+//     for what it takes; where they are few into tiles of equal height, which read a
+//     weight panel side by side and come out of the L2 together.  us, cut by 256 / equal
+//     heights: 8 experts of 1024 rows (28672 x 4096) 1610 / 1750, 128 ragged ones of 1024
+//     (4096 x 1536) 1525 / 1635; 256 of 256 rows (4096 x 7168) 4860 / 4460, 64 of 128
+//     (4096 x 2048) 268 / 248.
 //   - Gated: the tile's B rows are 128 of the gate and the same 128 of the up half,
 //     laid out so that a wavefront's two column halves are 32 channels' gate and up
 //     parts: both are in one lane's registers.
@@ -64,16 +72,18 @@ __device__ __forceinline__ u32x4 pack8_add(f32x4 v0, f32x4 v1, u32x4 r) {
   return u32x4{add(r[0], s0[0], s0[2]), add(r[1], s1[0], s1[2]), add(r[2], s0[1], s0[3]), add(r[3], s1[1], s1[3])};
 }
 
-template <bool GATED, bool PRE, bool RES>
+// GROUPED: the compact layout; else one matrix, whose tiles are whole but for one row of
+// them, so that leaving out a half would cost more (a branch a phase, 1%) than it gains.
+template <bool GROUPED, bool GATED, bool PRE, bool RES>
 __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  static_assert(!RES || !(GATED || PRE), "no store for gated ones; too many registers with pre");
+  static_assert(!RES || !(GROUPED || GATED || PRE), "no store for gated ones; too many registers with pre");
   // A half h of stage s, B of stage s.  Arrays of their own: the compiler then knows
   // which loads to LDS a read can depend on.
   __shared__ __attribute__((aligned(1024))) uint8_t p00[16384], p01[16384], p10[16384], p11[16384];
   __shared__ __attribute__((aligned(1024))) uint8_t q0[32768], q1[32768];
   __shared__ __attribute__((aligned(16))) uint8_t sbias[8 * 256];
-  __shared__ int4 table[runs::kTable];
+  __shared__ int4 table[GROUPED ? runs::kTable : 1];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -85,11 +95,11 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
 
   // ======== the tiles of this workgroup ========
   int pos, pos_end, stride, NR, cur = 0;
-  if (a.m_indices) {
+  if constexpr (GROUPED) {
     runs::Share sh;
     static_assert(runs::kMaxBlocks * 4 <= 32768, "the set-up arrays fit in the stages");
-    if (!runs::build_share<8, true>(a.m_indices, a.M, a.G, ntn, reinterpret_cast<int*>(q0),
-                                    reinterpret_cast<int*>(q1), reinterpret_cast<int*>(p00), table, sh))
+    if (!runs::build_share<8, true, true>(a.m_indices, a.M, a.G, ntn, reinterpret_cast<int*>(q0),
+                                    reinterpret_cast<int*>(q1), reinterpret_cast<int*>(p00), table, sh, a.deep != 0))
       return;
     NR = __builtin_amdgcn_readfirstlane(sh.NR);
     pos = __builtin_amdgcn_readfirstlane(sh.lo) + static_cast<int>(blockIdx.x >> 3);
@@ -106,12 +116,13 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
     pos_end = static_cast<int>((U * (xcd + 1)) >> 3);
     stride = gridDim.x >> 3;
   }
+  const int quantum = GROUPED && !a.deep ? 16 : runs::kTileRows;  // of a tile's rows
   // The workgroup's next tile; false: none left.
   auto fetch = [&](Tile& t) __attribute__((always_inline)) -> bool {
     int at = pos, c = cur;
     runs::Tile r;
     r.rows = 0;
-    for (; at < pos_end && r.rows <= 0; at += stride) r = runs::decode<16>(table, NR, c, at, fresh_copy(ntn));
+    for (; at < pos_end && r.rows <= 0; at += stride) r = runs::decode<16>(table, NR, c, at, fresh_copy(ntn), quantum);
     if (r.rows <= 0) return false;
     pos = at;
     cur = c;
@@ -131,17 +142,18 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
   int ahead = 0;  // tiles between the two
 
   // ======== load side ========
-  // A load fills 1 KB: eight rows of 128 bytes.
-  const uint32_t chunk = ((lane & 7) ^ (lane >> 3)) << 4;
+  // A load fills 1 KB: eight rows of 128 bytes, an even load (row & 8) == 0.
+  const uint32_t chunk[2] = {static_cast<uint32_t>(((lane & 7) ^ (lane >> 3)) << 4),
+                             static_cast<uint32_t>(((lane & 7) ^ (lane >> 3) ^ 1) << 4)};
   uint32_t vp[2], vq[4];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) vp[j] = static_cast<uint32_t>(((wave * 2 + j) * 8 + (lane >> 3)) * a.lda) + chunk;
+  for (int j = 0; j < 2; ++j) vp[j] = static_cast<uint32_t>(((wave * 2 + j) * 8 + (lane >> 3)) * a.lda) + chunk[j & 1];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     int r = (wave * 4 + j) * 8 + (lane >> 3);
     // gated: 32 gate rows, then the up rows of the same channels, for each column wavefront
     if constexpr (GATED) r = (r >> 6) * 32 + (r & 31) + ((r >> 5) & 1) * a.cols;
-    vq[j] = static_cast<uint32_t>(r * ldb) + chunk;
+    vq[j] = static_cast<uint32_t>(r * ldb) + chunk[j & 1];
   }
   const uint8_t *bp, *bq;  // this step's operands
   int np, np1;             // bytes within bounds of A's halves
@@ -201,7 +213,7 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
   uint32_t op[2], oq[2];  // LDS offsets of this lane's part of a fragment
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const uint32_t c = ((2 * fg + k) ^ (fr & 7)) << 4;
+    const uint32_t c = ((2 * fg + k) ^ (fr & 7) ^ (fr >> 3)) << 4;
     op[k] = (wm * 64 + fr) * 128 + c;
     oq[k] = (wn * 64 + fr) * 128 + c;
   }
@@ -215,7 +227,7 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
   };
   bf16x8 fp[2][4];     // A half in use: [k half][16-row block]
   bf16x8 fq[2][2][2];  // B half: [half][k half][16-column block]
-  f32x4 acc[2][2][4][2] = {};
+  f32x4 acc[2][2][4][2];
   auto read_p = [&](const uint8_t* s) __attribute__((always_inline)) {
 #pragma unroll
     for (int k = 0; k < 2; ++k)
@@ -229,7 +241,8 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
       for (int j = 0; j < 2; ++j) fq[h][k][j] = *reinterpret_cast<const bf16x8*>(s + oq[k] + h * 4096 + j * 2048);
   };
   // D^T: a lane ends with four consecutive columns of one row
-  auto mma = [&](int hp, int hq) __attribute__((always_inline)) {
+  // (a tile's first products start from zero, which saves clearing the accumulators)
+  auto mma = [&](int hp, int hq, auto fresh) __attribute__((always_inline)) {
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int k = 0; k < 2; ++k)
@@ -237,7 +250,8 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          acc[hp][hq][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[hq][k][j], fp[k][i], acc[hp][hq][i][j], 0, 0, 0);
+          acc[hp][hq][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              fq[hq][k][j], fp[k][i], decltype(fresh)::value && k == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[hp][hq][i][j], 0, 0, 0);
     __builtin_amdgcn_s_setprio(0);
   };
 
@@ -259,7 +273,7 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
                                              in ? static_cast<uint32_t>(c * es) : 0x7ffffff0u, 0, 0, 0);
   };
 
-  // Outputs of the finished tile, then zero accumulators.  Every wavefront issues the
+  // Outputs of the finished tile.  Every wavefront issues the
   // same number of stores whatever its tile holds (rows and columns outside fall
   // outside the buffer and are dropped), so that the waits of the next two steps can
   // count them.
@@ -269,8 +283,8 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
     int l = lane;
     asm volatile("" : "+v"(l));
     const int row = l & 15, g = l >> 4;
-    f32x4 bias[2][2];
-    {
+    if (a.bias) {
+      f32x4 bias[2][2];
       // read by hand: the compiler would wait for all loads in flight.  This one was
       // issued before the tile's first step.
       const uint32_t at = runs::lds_off(bias_lds) + g * (a.bias32 ? 16 : 8);
@@ -286,12 +300,21 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
 #pragma unroll
         for (int q = 0; q < 4; ++q) bias[q >> 1][q & 1] = unpack_bf16x4(b[q]);
       }
+#pragma unroll
+      for (int hp = 0; hp < 2; ++hp)
+#pragma unroll
+        for (int hq = 0; hq < 2; ++hq)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc[hp][hq][i][j] += bias[hq][j];
     }
     const int c0 = ct.nt * kCols + wn * (GATED ? 32 : 64);
     const int cols = fresh_copy(a.cols), N = fresh_copy(a.N);
     const int oline = static_cast<int>(a.ldo) * 2, pline = N * 2;
-    // columns of a lane's 16 bytes: of 64 (whole lines, eight rows a store) and of 32 (16 rows)
-    const uint32_t o64 = ((g & 1) * 16 + (g >> 1) * 8 + (row >> 3) * 32) * 2, r64 = row & 7;
+    // of a lane's 16 bytes in a half's 64: a store covers 16 rows.  (Whole lines of eight
+    // rows take an exchange between lanes, which costs more than the stores gain: 4096 x
+    // 1536, 16384 rows, us 162 and 160, with GELU 202 and 198.)
     const uint32_t o32 = ((g & 1) * 16 + (g >> 1) * 8) * 2;
     // the lines of the quadrants' 64 rows from column col on
     const auto part = [&](const void* p, int64_t line, int hp, int col) __attribute__((always_inline)) {
@@ -312,18 +335,12 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            old[hp][i][h] = __builtin_amdgcn_raw_buffer_load_b128(rr, (i * 16 + h * 8 + r64) * rline + o64, 0, 0);
+            old[hp][i][h] = __builtin_amdgcn_raw_buffer_load_b128(rr, (i * 16 + row) * rline + o32 + h * 64, 0, 0);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int hp = 0; hp < 2; ++hp) {
-#pragma unroll
-      for (int hq = 0; hq < 2; ++hq)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) acc[hp][hq][i][j] += bias[hq][j];
       if constexpr (GATED) {
         if constexpr (PRE) {
           const auto rg = part(a.pre, pline, hp, c0), ru = part(a.pre, pline, hp, c0 + cols);
@@ -350,39 +367,26 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
             u32x4 w[2];
 #pragma unroll
             for (int hq = 0; hq < 2; ++hq) w[hq] = pack8(acc[hp][hq][i][0], acc[hp][hq][i][1]);
-            trade8(w[0], w[1]);
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              __builtin_amdgcn_raw_buffer_store_b128(w[h], rd, (i * 16 + h * 8 + r64) * pline + o64, 0, 0);
+              __builtin_amdgcn_raw_buffer_store_b128(w[h], rd, (i * 16 + row) * pline + o32 + h * 64, 0, 0);
           }
         }
         const auto rd = part(a.out, oline, hp, c0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           u32x4 w[2];
-          if constexpr (RES) trade8(old[hp][i][0], old[hp][i][1]);
 #pragma unroll
           for (int hq = 0; hq < 2; ++hq) {
             const f32x4 v0 = act::value4(a.act, acc[hp][hq][i][0]), v1 = act::value4(a.act, acc[hp][hq][i][1]);
             w[hq] = RES ? pack8_add(v0, v1, old[hp][i][hq]) : pack8(v0, v1);
           }
-          trade8(w[0], w[1]);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            __builtin_amdgcn_raw_buffer_store_b128(w[h], rd, (i * 16 + h * 8 + r64) * oline + o64, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(w[h], rd, (i * 16 + row) * oline + o32 + h * 64, 0, 0);
         }
       }
     }
-    float zero = 0.0f;  // in a vector register: as constants, 128 scalar ones are taken for it
-    asm volatile("" : "+v"(zero));
-#pragma unroll
-    for (int hp = 0; hp < 2; ++hp)
-#pragma unroll
-      for (int hq = 0; hq < 2; ++hq)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) acc[hp][hq][i][j] = f32x4{zero, zero, zero, zero};
   };
 
   // ======== the stream ========
@@ -393,16 +397,18 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
   // before the first one reads.
   constexpr int kStores = (GATED ? 8 : 16) + (PRE ? 16 : 0) + 1;
   constexpr int kW1 = 10 + kStores < 63 ? 10 + kStores : 63, kW2 = 8 + kStores < 63 ? 8 + kStores : 63;
+  bool half = false;  // the tile has no rows in its lower half
   // One step from stage S, starting with B's half S.
   auto step = [&](uint8_t* ps0, uint8_t* ps1, uint8_t* qs, uint8_t* qn, auto S_, auto first_) __attribute__((always_inline)) {
     constexpr int S = decltype(S_)::value;
     constexpr bool first = decltype(first_)::value;
+    constexpr std::integral_constant<bool, first && S == 0> fresh{};
     // phase 0
     hold();
     read_p(ps0);
     wait_lds();
     barrier();
-    mma(0, S);
+    mma(0, S, fresh);
     barrier();
     // phase 1: A half 0 of this stage is free
     read_q(qs, 1 - S);
@@ -411,16 +417,16 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
     fence();
     wait_vm<first ? kW1 : 10>();  // A half 1 of this step
     barrier();
-    mma(0, 1 - S);
+    mma(0, 1 - S, fresh);
     barrier();
     // phase 2: so is B
-    read_p(ps1);
+    if (!GROUPED || !half) read_p(ps1);
     load_q(qs);
     wait_lds();
     fence();
     wait_vm<first && S == 0 ? kW2 : 8>();  // B and A half 0 of the next step
     barrier();
-    mma(1, 1 - S);
+    if (!GROUPED || !half) mma(1, 1 - S, fresh);
     barrier();
     // phase 3
     read_q(qn, 1 - S);
@@ -428,7 +434,7 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
     advance();
     wait_lds();
     barrier();
-    mma(1, S);
+    if (!GROUPED || !half) mma(1, S, fresh);
     barrier();
   };
   using std::integral_constant;
@@ -454,6 +460,7 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
   barrier();
   if (wm == 1) __builtin_amdgcn_s_barrier();  // half a phase behind
   for (;;) {
+    half = ct.rows <= 128;
     pair(integral_constant<bool, true>());
     for (int s = 2; s < steps; s += 2) pair(integral_constant<bool, false>());
     fence();
@@ -483,11 +490,11 @@ int grid_size() {
   return grid[dev];
 }
 
-template <bool GATED, bool PRE, bool RES>
+template <bool GROUPED, bool GATED, bool PRE, bool RES = false>
 int32_t launch(const LinearArgs& a, hipStream_t s) {
   const int grid = grid_size();
   if (grid == 0) return MOE_EDEVICE;
-  linear_wide_kernel<GATED, PRE, RES><<<grid, kThreads, 0, s>>>(a);
+  linear_wide_kernel<GROUPED, GATED, PRE, RES><<<grid, kThreads, 0, s>>>(a);
   MOE_CHECK_LAUNCH();
   return MOE_OK;
 }
@@ -496,7 +503,7 @@ int32_t launch(const LinearArgs& a, hipStream_t s) {
 
 bool linear_wide_covers(const LinearArgs& a) {
   const int64_t ldb = static_cast<int64_t>(a.K) * 2;
-  return !a.out32 && a.vec8 && !(a.residual && (a.act.gated || a.pre)) && a.K % kStep == 0 && a.K >= 2 * kStep && a.cols % 64 == 0 &&
+  return !a.out32 && a.vec8 && !(a.residual && (a.m_indices || a.act.gated || a.pre)) && a.K % kStep == 0 && a.K >= 2 * kStep && a.cols % 64 == 0 &&
          // 32-bit offsets: 256 rows of A, out and pre, of B 256 rows or (gated) half of all
          a.lda <= (1 << 22) && a.ldo <= (1 << 21) && a.ldr <= (1 << 21) && a.N <= (1 << 21) &&
          (a.act.gated ? (static_cast<int64_t>(a.cols) + 256) * ldb < (1ll << 32) : a.K <= (1 << 21)) &&
@@ -506,9 +513,13 @@ bool linear_wide_covers(const LinearArgs& a) {
 }
 
 int32_t launch_linear_wide(const LinearArgs& a, hipStream_t s) {
-  if (a.act.gated) return a.pre ? launch<true, true, false>(a, s) : launch<true, false, false>(a, s);
-  if (a.residual) return launch<false, false, true>(a, s);
-  return a.pre ? launch<false, true, false>(a, s) : launch<false, false, false>(a, s);
+  if (a.m_indices) {
+    if (a.act.gated) return a.pre ? launch<true, true, true>(a, s) : launch<true, true, false>(a, s);
+    return a.pre ? launch<true, false, true>(a, s) : launch<true, false, false>(a, s);
+  }
+  if (a.act.gated) return a.pre ? launch<false, true, true>(a, s) : launch<false, true, false>(a, s);
+  if (a.residual) return launch<false, false, false, true>(a, s);
+  return a.pre ? launch<false, false, true>(a, s) : launch<false, false, false>(a, s);
 }
 
 }  // namespace moe

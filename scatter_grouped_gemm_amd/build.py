@@ -19,7 +19,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["route.hip", "scatter.hip", "quant.hip", "combine.hip", "gemm.hip", "gemm_act.hip", "gemm_wreg.hip",
            "token_grad.hip", "silu_bwd.hip", "gemm_grad.hip", "dgrad_short.hip", "wgrad_short.hip",
-           "adamw.hip", "linear.hip", "linear_wide.hip", "act_bwd.hip"]
+           "adamw.hip", "linear.hip", "linear_wide.hip", "linear_thin.hip", "act_bwd.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",

@@ -27,9 +27,15 @@ struct LinearArgs {
 // The kernel that the sizes ask for; arguments are checked by the caller.
 int32_t launch_linear(const LinearArgs& a, hipStream_t stream);
 
+// CUs of the current device, rounded down to a multiple of 8; 0: an error.
+int linear_cus();
+
 // linear_wide.hip: whether it covers the call, and the launch.
 bool linear_wide_covers(const LinearArgs& a);
 int32_t launch_linear_wide(const LinearArgs& a, hipStream_t stream);
+
+// linear_thin.hip: of one matrix and few rows.
+int32_t launch_linear_thin(const LinearArgs& a, hipStream_t stream);
 
 // Sets vec and vec8 from the other fields.
 void linear_alignment(LinearArgs& a);

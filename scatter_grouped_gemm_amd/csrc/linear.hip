@@ -1,5 +1,7 @@
-// Dense product with bias, activation and residual in its epilogue (moe_linear):
-// tiles of BM rows by BN columns of B, four wavefronts of BM/2 by BN/2.
+// Products with bias, activation and residual in their epilogue: tiles of BM rows by BN
+// rows of B, four wavefronts of BM/2 by BN/2, for the dense product (moe_linear) and the
+// compact grouped one, where it is too small for linear_wide.hip or has a form that that
+// kernel does not (any N, K a multiple of 8, fp32 output, rows apart).
 //
 // The sum of an output runs through v_mfma_f32_16x16x32_bf16 over ascending k; a
 // step of 64 takes the 16-byte chunks 0, 2, 4, 6 of a row's 128 bytes in its first
@@ -7,11 +9,16 @@
 // output has the same bits from every kernel.
 //   - Loads go straight to LDS (16 bytes a lane), a stage holds a step's rows of A
 //     and B; chunks are permuted within a row so that the 16 lanes of a fragment
-//     read hit different banks.  Three stages, two steps in flight.
+//     read hit different banks.  The next step's fragments are read while a step's MFMAs
+//     run.  What bounds a tile by itself is LDS: a 64 x 64 step (0.29 us) reads 32 KB
+//     from it and writes 16; deeper stages change nothing.
+//   - The order of the tiles keeps those that share rows on one XCD: 8192 rows, K 7168, N
+//     256 46 us, dealt over all of them 68 (each L2 then reads A).
 //   - Whatever lies outside (rows behind the last, k behind K) is read as 0 through
 //     the bounds of the buffer descriptor: a lane's offset is moved out of it.
 //   - Gated: a wavefront holds BN/4 gate columns and the same channels of the up
 //     half, so that both are in one lane's registers.
+#include "gemm_runs.h"
 #include "grad_tile.h"
 #include "linear.h"
 
@@ -20,20 +27,31 @@ namespace {
 
 constexpr uint32_t kOutside = 0xfffffff0u;  // beyond any descriptor here
 
-template <int BM, int BN, bool GATED>
+template <int BM, int BN, int S, bool GATED>
 __global__ __launch_bounds__(256, 2) void linear_tile_kernel(const LinearArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int WM = BM / 2, WN = BN / 2, TM = WM / 16, TN = WN / 16;
   constexpr int LA = BM / 32, LB = BN / 32;  // 1 KB loads of a wavefront and step
   constexpr int NC = GATED ? BN / 2 : BN;    // output columns of a tile
-  __shared__ __attribute__((aligned(1024))) uint8_t s0[(BM + BN) * 128], s1[(BM + BN) * 128], s2[(BM + BN) * 128];
+  constexpr int STAGE = (BM + BN) * 128;
+  static_assert(LA % 2 == 0 && LB % 2 == 0, "whole pairs of loads");
+  static_assert((S == 2 || S == 4) && (LA + LB) * (S - 2) < 64, "loads in flight");
+  // Arrays of their own: the compiler then knows which loads to LDS a read can depend on.
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[STAGE], s1[STAGE], s2[S > 2 ? STAGE : 1], s3[S > 2 ? STAGE : 1];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   const int fr = lane & 15, fg = lane >> 4;
-  const int nct = (a.cols + NC - 1) / NC;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x / nct) * BM;
-  const int col0 = static_cast<int>(blockIdx.x % nct) * NC;
+  // Workgroup ids are dealt round-robin over the XCDs, each with its own L2: an XCD takes
+  // a contiguous eighth of the order, in which eight tile columns go down the rows
+  // together, so that what runs at the same time shares rows of both operands.
+  const int nct = (a.cols + NC - 1) / NC, nrt = static_cast<int>((a.M + BM - 1) / BM);
+  const int tile = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+  if (tile >= nrt * nct) return;
+  const int cg = tile / (8 * nrt) * 8, in_group = tile - cg * nrt;
+  const int cw = nct - cg < 8 ? nct - cg : 8;
+  const int64_t row0 = static_cast<int64_t>(in_group / cw) * BM;
+  const int col0 = (cg + in_group % cw) * NC;
   int e = 0, rows = a.M - row0 < BM ? static_cast<int>(a.M - row0) : BM;
   if (a.m_indices) {  // a block of 128 rows has one expert, and its valid rows come first
     e = __builtin_amdgcn_readfirstlane(a.m_indices[row0]);
@@ -48,11 +66,12 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(const LinearArgs a)
   // Offsets of this lane's 16 bytes from the tile's first row of A and of B (below 2^32
   // by the limits of the call).
   uint32_t va[LA], vb[LB];
-  const int chunk = (lane & 7) ^ (lane >> 3);  // of the row's 128 bytes: a load covers 8 rows
+  // 16-byte chunk of the row's 128: a load covers 8 rows, an even one those with (row & 8) == 0
+  const int chunk[2] = {(lane & 7) ^ (lane >> 3), (lane & 7) ^ (lane >> 3) ^ 1};
 #pragma unroll
   for (int j = 0; j < LA; ++j) {
     const int r = (wave * LA + j) * 8 + (lane >> 3);
-    va[j] = r < rows ? static_cast<uint32_t>(r * a.lda) + chunk * 16 : kOutside;
+    va[j] = r < rows ? static_cast<uint32_t>(r * a.lda) + chunk[j & 1] * 16 : kOutside;
   }
 #pragma unroll
   for (int j = 0; j < LB; ++j) {
@@ -67,78 +86,103 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(const LinearArgs a)
       n = r;
       in = col0 + r < a.N;
     }
-    vb[j] = in ? static_cast<uint32_t>(n * ldb) + chunk * 16 : kOutside;
+    vb[j] = in ? static_cast<uint32_t>(n * ldb) + chunk[j & 1] * 16 : kOutside;
   }
-  const uint8_t* pa = a.A + row0 * a.lda;
-  const uint8_t* pb = a.B + (static_cast<int64_t>(e) * a.N + col0) * ldb;
-  const int na = rows * static_cast<int>(a.lda);       // bytes of the tile's rows
-  int nr = GATED ? a.cols + NC : BN;                    // B rows that the tile's offsets reach
+  int nr = GATED ? a.cols + NC : BN;  // B rows that the tile's offsets reach
   nr = nr < a.N - col0 ? nr : a.N - col0;
-  const uint32_t nb = static_cast<uint32_t>(nr * ldb);
-  const int steps = (a.K + kStep - 1) / kStep;
-  int loaded = 0;
+  const auto ra = buffer(a.A + row0 * a.lda, rows * static_cast<int>(a.lda));
+  const auto rb = buffer_u(a.B + (static_cast<int64_t>(e) * a.N + col0) * ldb, static_cast<uint32_t>(nr * ldb));
+  auto to_lds = [&](__amdgpu_buffer_rsrc_t rs, uint8_t* dst, uint32_t off, int more) __attribute__((always_inline)) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16, off, more, 0, 0);
+  };
+  const int steps = (a.K + kStep - 1) / kStep, whole = a.K / kStep;
+  int next = 0;  // step to be loaded
+  // The same number of loads in every step; of what lies behind K nothing is read.
   auto load = [&](uint8_t* s) __attribute__((always_inline)) {
-    // behind the last step nothing is read, but the same number of loads is issued
-    const int left = a.K - loaded * kStep;
-    const bool in = chunk * 8 < left;
-    const auto ra = buffer(pa, left > 0 ? na - loaded * (kStep * 2) : 0), rb = buffer_u(pb, left > 0 ? nb - loaded * (kStep * 2) : 0);
+    const int at = next * (kStep * 2);
+    if (next < whole) {
 #pragma unroll
-    for (int j = 0; j < LA; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (__attribute__((address_space(3))) void*)(s + (wave * LA + j) * 1024), 16,
-                                               in ? va[j] : kOutside, 0, 0, 0);
+      for (int j = 0; j < LA; ++j) to_lds(ra, s + (wave * LA + j) * 1024, va[j], at);
 #pragma unroll
-    for (int j = 0; j < LB; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (__attribute__((address_space(3))) void*)(s + BM * 128 + (wave * LB + j) * 1024), 16,
-                                               in ? vb[j] : kOutside, 0, 0, 0);
-    pa += kStep * 2;
-    pb += kStep * 2;
-    ++loaded;
+      for (int j = 0; j < LB; ++j) to_lds(rb, s + BM * 128 + (wave * LB + j) * 1024, vb[j], at);
+    } else {
+      const int left = a.K - next * kStep;
+      const bool in[2] = {chunk[0] * 8 < left, chunk[1] * 8 < left};
+#pragma unroll
+      for (int j = 0; j < LA; ++j) to_lds(ra, s + (wave * LA + j) * 1024, in[j & 1] && va[j] != kOutside ? va[j] + at : kOutside, 0);
+#pragma unroll
+      for (int j = 0; j < LB; ++j)
+        to_lds(rb, s + BM * 128 + (wave * LB + j) * 1024, in[j & 1] && vb[j] != kOutside ? vb[j] + at : kOutside, 0);
+    }
+    ++next;
   };
   uint32_t oa[2], ob[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const int c = ((2 * fg + k) ^ (fr & 7)) << 4;
+    const int c = ((2 * fg + k) ^ (fr & 7) ^ (fr >> 3)) << 4;
     oa[k] = (wm * WM + fr) * 128 + c;
     ob[k] = (BM + wn * WN + fr) * 128 + c;
   }
-  f32x4 acc[TN][TM] = {};
-  auto step = [&](uint8_t* s, uint8_t* next) __attribute__((always_inline)) {
-    fence();
-    wait_vm<LA + LB>();  // this step's loads, of two steps'
-    barrier();           // everyone's, and everyone has read the step before
-    load(next);
+  struct Frags {
+    bf16x8 a[2][TM], b[2][TN];
+  } f0, f1;
+  auto read = [&](Frags& f, const uint8_t* s) __attribute__((always_inline)) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      bf16x8 fa[TM], fb[TN];
 #pragma unroll
-      for (int i = 0; i < TM; ++i) fa[i] = *reinterpret_cast<const bf16x8*>(s + oa[k] + i * 2048);
+      for (int i = 0; i < TM; ++i) f.a[k][i] = *reinterpret_cast<const bf16x8*>(s + oa[k] + i * 2048);
 #pragma unroll
-      for (int j = 0; j < TN; ++j) fb[j] = *reinterpret_cast<const bf16x8*>(s + ob[k] + j * 2048);
+      for (int j = 0; j < TN; ++j) f.b[k][j] = *reinterpret_cast<const bf16x8*>(s + ob[k] + j * 2048);
+    }
+  };
+  f32x4 acc[TN][TM] = {};
+  // A step whose fragments are in f: the next step's are read into g while its MFMAs
+  // run, and its stage is filled again.
+  auto step = [&](Frags& f, Frags& g, uint8_t* stage, const uint8_t* following) __attribute__((always_inline)) {
+    wait_lds();
+    fence();
+    wait_vm<(LA + LB) * (S - 2)>();  // the next step's loads
+    barrier();                       // everyone's, and everyone has read this stage
+    read(g, following);
+    load(stage);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
       for (int j = 0; j < TN; ++j)
 #pragma unroll
-        for (int i = 0; i < TM; ++i) acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[j][i], 0, 0, 0);
-    }
-    wait_lds();
+        for (int i = 0; i < TM; ++i)
+          acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.b[k][j], f.a[k][i], acc[j][i], 0, 0, 0);
   };
   load(s0);
   load(s1);
+  if constexpr (S > 2) {
+    load(s2);
+    load(s3);
+  }
+  fence();
+  wait_vm<(LA + LB) * (S - 1)>();
+  barrier();
+  read(f0, s0);
   for (int t = 0;;) {
-    step(s0, s2);
+    step(f0, f1, s0, s1);
     if (++t >= steps) break;
-    step(s1, s0);
+    step(f1, f0, s1, S > 2 ? s2 : s0);
     if (++t >= steps) break;
-    step(s2, s1);
-    if (++t >= steps) break;
+    if constexpr (S > 2) {
+      step(f0, f1, s2, s3);
+      if (++t >= steps) break;
+      step(f1, f0, s3, s0);
+      if (++t >= steps) break;
+    }
   }
   fence();
   wait_vm<0>();  // the loads behind the last step write LDS too
 
   constexpr int TH = GATED ? TN / 2 : TN;
-  const int cw = col0 + wn * (GATED ? WN / 2 : WN) + fg * 4;
+  const int c0 = col0 + wn * (GATED ? WN / 2 : WN) + fg * 4;
 #pragma unroll
   for (int j = 0; j < TH; ++j) {
-    const int n = cw + j * 16;
+    const int n = c0 + j * 16;
     const f32x4 bg = bias4(a, e, n, a.cols);
     f32x4 bu{};
     if constexpr (GATED)
@@ -152,17 +196,18 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(const LinearArgs a)
 #endif
 }
 
-template <int BM, int BN>
+template <int BM, int BN, int S, bool GATED>
 int32_t launch(const LinearArgs& a, hipStream_t s) {
-  const int nc = a.act.gated ? BN / 2 : BN;
+  constexpr int nc = GATED ? BN / 2 : BN;
   const int64_t tiles = (a.M + BM - 1) / BM * ((a.cols + nc - 1) / nc);
   if (tiles >= (1 << 24)) return MOE_EUNSUPPORTED;  // threads of a launch
-  if (a.act.gated)
-    linear_tile_kernel<BM, BN, true><<<static_cast<unsigned>(tiles), 256, 0, s>>>(a);
-  else
-    linear_tile_kernel<BM, BN, false><<<static_cast<unsigned>(tiles), 256, 0, s>>>(a);
+  linear_tile_kernel<BM, BN, S, GATED><<<static_cast<unsigned>((tiles + 7) / 8 * 8), 256, 0, s>>>(a);
   MOE_CHECK_LAUNCH();
   return MOE_OK;
+}
+template <int BM, int BN, int S>
+int32_t launch(const LinearArgs& a, hipStream_t s) {
+  return a.act.gated ? launch<BM, BN, S, true>(a, s) : launch<BM, BN, S, false>(a, s);
 }
 
 inline bool aligned(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
@@ -178,11 +223,26 @@ void linear_alignment(LinearArgs& a) {
            (!a.residual || (a.ldr % 8 == 0 && aligned(a.residual, 16))) && (!a.pre || aligned(a.pre, 16));
 }
 
+// Which kernel takes a call, by the tiles that each would have; the bits are the same.
+// us, one matrix, K 4096 (7168 where marked):
+//   up to 32 rows, the thin kernel: 1 row, N 4096* 12 (64 x 64 tiles 32), N 16384* 35 (40);
+//     with wider N the 64 x 64 tiles' reads are as good, and they read A less often (32
+//     rows, N 28672 43 / 35)
+//   256 x 256 tiles for more than half of the CUs: 128 tiles 76 (128 x 128 ones 74), 160
+//     78 (108), 256 96 (123)
+//   128 x 128 for three tiles for two CUs and up, two workgroups a CU: 448 tiles 62 (128 x
+//     64 92, 64 x 64 87)
+//   64 x 64 up to two tiles a CU: 64 tiles* 33 (128 x 64 49, 128 x 128 73), 512 tiles* (N
+//     256) 46 (53, 78)
+//   128 x 64 between them: 512 tiles* 75 (128 x 128 76, 64 x 64 88)
 int32_t launch_linear(const LinearArgs& a, hipStream_t s) {
-  const int64_t n = a.N;
-  if (linear_wide_covers(a) && (a.M + 255) / 256 * ((n + 255) / 256) >= 200) return launch_linear_wide(a, s);
-  // tiles of 128 x 128 where they fill the card
-  return (a.M + 127) / 128 * ((n + 127) / 128) >= 256 ? launch<128, 128>(a, s) : launch<64, 64>(a, s);
+  const int64_t cus = linear_cus(), n = a.N;
+  if (cus == 0) return MOE_EDEVICE;
+  if (!a.m_indices && a.M <= 32 && n <= 16384) return launch_linear_thin(a, s);
+  if (linear_wide_covers(a) && 2 * ((a.M + 255) / 256 * ((n + 255) / 256)) > cus) return launch_linear_wide(a, s);
+  if (2 * ((a.M + 127) / 128 * ((n + 127) / 128)) >= 3 * cus) return launch<128, 128, 2>(a, s);
+  if ((a.M + 63) / 64 * ((n + 63) / 64) <= 2 * cus) return launch<64, 64, 4>(a, s);
+  return launch<128, 64, 2>(a, s);
 }
 
 }  // namespace moe

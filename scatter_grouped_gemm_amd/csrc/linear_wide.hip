@@ -476,8 +476,19 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
 #endif
 }
 
-// One workgroup per CU, a multiple of 8 (one share of the tiles per XCD).
-int grid_size() {
+template <bool GROUPED, bool GATED, bool PRE, bool RES = false>
+int32_t launch(const LinearArgs& a, hipStream_t s) {
+  const int grid = linear_cus();  // one workgroup per CU
+  if (grid == 0) return MOE_EDEVICE;
+  linear_wide_kernel<GROUPED, GATED, PRE, RES><<<grid, kThreads, 0, s>>>(a);
+  MOE_CHECK_LAUNCH();
+  return MOE_OK;
+}
+
+}  // namespace
+
+// CUs of the current device, a multiple of 8 (one share of the tiles per XCD).
+int linear_cus() {
   static int grid[64] = {0};
   static std::once_flag once[64];
   int dev = 0;
@@ -489,17 +500,6 @@ int grid_size() {
   });
   return grid[dev];
 }
-
-template <bool GROUPED, bool GATED, bool PRE, bool RES = false>
-int32_t launch(const LinearArgs& a, hipStream_t s) {
-  const int grid = grid_size();
-  if (grid == 0) return MOE_EDEVICE;
-  linear_wide_kernel<GROUPED, GATED, PRE, RES><<<grid, kThreads, 0, s>>>(a);
-  MOE_CHECK_LAUNCH();
-  return MOE_OK;
-}
-
-}  // namespace
 
 bool linear_wide_covers(const LinearArgs& a) {
   const int64_t ldb = static_cast<int64_t>(a.K) * 2;

@@ -522,7 +522,7 @@ int32_t silu_and_mul_bwd(const void* gateup, const void* dact, int64_t M, int32_
                          void* dgateup, void* act, void* stream);
 
 /* Scratch bytes moe_act_bwd needs for dbias (G = 1 without a layout): sums of
- * blocks of rows.  0 on a negative or zero size. */
+ * blocks of rows.  0 where it needs none (few rows), and on a negative or zero size. */
 size_t moe_act_bwd_ws_bytes(int64_t M, int32_t N, int32_t G);
 
 /* Gradient of the epilogue of moe_linear and grouped_gemm_*_act (the residual's
@@ -543,7 +543,8 @@ size_t moe_act_bwd_ws_bytes(int64_t M, int32_t N, int32_t G);
  *   expert_start_loc, num_valid   device int32 [G], needed with m_indices and dbias
  *   dbias        dbias_dtype MOE_DTYPE_BF16 or MOE_DTYPE_FP32 [G][N], or NULL.  An
  *                expert without rows gets 0 (or keeps what it holds)
- *   ws, ws_bytes scratch for dbias, at least moe_act_bwd_ws_bytes(M, N, G)
+ *   ws, ws_bytes scratch for dbias, at least moe_act_bwd_ws_bytes(M, N, G); calls that
+ *                may run at the same time need one each
  * Limits: N % 8 == 0 (16 with a gated activation), N <= 2^27, M < 2^26, G <= 65535;
  * pointers of tensors 16-byte aligned. */
 int32_t moe_act_bwd(const void* pre, const void* dout, int64_t M, int32_t N, int32_t act,

@@ -579,8 +579,12 @@ def moe_act_bwd(pre, dout, dpre, act, dbias=None, m_indices=None, expert_start_l
         ddt = MOE_DTYPE_FP32 if dbias.dtype is _F32 else MOE_DTYPE_BF16
         pd = _dev("dbias", dbias.dtype, (N,) if dbias.dim() == 1 and G == 1 else (G, N), dbias, dev)
         if ws is None:
-            ws = torch.empty(moe_act_bwd_ws_bytes(M, N, G), dtype=torch.uint8, device=dout.device)
-        pw, nw = _dev("ws", ws.dtype, ws.shape, ws, dev), ws.numel() * ws.element_size()
+            nw = moe_act_bwd_ws_bytes(M, N, G)
+            if nw:
+                ws = torch.empty(nw, dtype=torch.uint8, device=dout.device)
+                pw = ws.data_ptr()
+        else:
+            pw, nw = _dev("ws", ws.dtype, ws.shape, ws, dev), ws.numel() * ws.element_size()
     _check("moe_act_bwd", lib().moe_act_bwd(
         None if pre is None else _dev("pre", _BF16, (M, N), pre, dev), _dev("dout", _BF16, (M, cols), dout, dev), M, N, code,
         alpha, limit, None if m_indices is None else _dev("m_indices", _INT32, (M,), m_indices, dev),

@@ -70,7 +70,7 @@ def test_grouped_refusals_of_one_layout():
     assert contig(M=8177 * 128) == L.MOE_EUNSUPPORTED
 
 
-def bwd(pre=P, dout=P, M=256, N=256, act=9, alpha=1.702, limit=7.0, m=None, mm=None, max_m=0, st=None, nv=None, G=1,
+def bwd(pre=P, dout=P, M=2560, N=256, act=9, alpha=1.702, limit=7.0, m=None, mm=None, max_m=0, st=None, nv=None, G=1,
         dpre=P, ddt=16, acc=0, db=None, ws=P, nws=1 << 30):
     return L.lib().moe_act_bwd(pre, dout, M, N, act, alpha, limit, m, mm, max_m, st, nv, G, dpre, ddt, acc, db, ws, nws, None)
 
@@ -91,10 +91,10 @@ def test_act_bwd_refusals(kw, want):
 
 
 def test_act_bwd_ws_bytes():
-    for M, N, G in [(1, 16, 1), (8191, 4096, 1), (131072, 28672, 256)]:
+    for M, N, G in [(129, 16, 1), (8191, 4096, 1), (131072, 28672, 256)]:
         n = L.moe_act_bwd_ws_bytes(M, N, G)
         assert n >= -(-M // 16) * N * 4 and n % 4 == 0
-    for bad in [(0, 16, 1), (16, 0, 1), (16, 16, 0), (-1, 16, 1)]:
+    for bad in [(0, 16, 1), (160, 0, 1), (160, 16, 0), (-1, 16, 1), (128, 16, 1), (1024, 4096, 8)]:   # the last two need none
         assert L.moe_act_bwd_ws_bytes(*bad) == 0
 
 

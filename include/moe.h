@@ -536,10 +536,11 @@ size_t moe_act_bwd_ws_bytes(int64_t M, int32_t N, int32_t G);
  *   Rows: m_indices (compact), masked_m with max_m (masked; M = G*max_m) or, both
  *   NULL, every row (then G = 1).  Other rows of dpre are left as they were and are
  *   part of no sum.
- *   pre, dpre    bf16 [M][N]; dpre may be pre, and may be dout where the activation
- *                is not gated.  With MOE_ACT_NONE pre is not read, and dpre may be
+ *   pre, dpre    bf16 [M][N]; dpre may be pre, and may be a bf16 dout where the
+ *                activation is not gated.  With MOE_ACT_NONE pre is not read, and dpre may be
  *                NULL: the bias gradient alone
- *   dout         bf16 [M][N], [M][N/2] with a gated activation
+ *   dout         dout_dtype MOE_DTYPE_BF16 or MOE_DTYPE_FP32 (as the output was): [M][N],
+ *                [M][N/2] with a gated activation
  *   expert_start_loc, num_valid   device int32 [G], needed with m_indices and dbias
  *   dbias        dbias_dtype MOE_DTYPE_BF16 or MOE_DTYPE_FP32 [G][N], or NULL.  An
  *                expert without rows gets 0 (or keeps what it holds)
@@ -547,8 +548,8 @@ size_t moe_act_bwd_ws_bytes(int64_t M, int32_t N, int32_t G);
  *                may run at the same time need one each
  * Limits: N % 8 == 0 (16 with a gated activation), N <= 2^27, M < 2^26, G <= 65535;
  * pointers of tensors 16-byte aligned. */
-int32_t moe_act_bwd(const void* pre, const void* dout, int64_t M, int32_t N, int32_t act,
-                    float alpha, float limit, const int32_t* m_indices, const int32_t* masked_m,
+int32_t moe_act_bwd(const void* pre, int32_t dout_dtype, const void* dout, int64_t M, int32_t N,
+                    int32_t act, float alpha, float limit, const int32_t* m_indices, const int32_t* masked_m,
                     int32_t max_m, const int32_t* expert_start_loc, const int32_t* num_valid,
                     int32_t G, void* dpre, int32_t dbias_dtype, int32_t accumulate, void* dbias,
                     void* ws, size_t ws_bytes, void* stream);

@@ -70,7 +70,7 @@ SIGNATURES = {
     "grouped_gemm_masked_act": (_I32, [_I32, _P, _P, _P, _P, _P, _I32, _I32, _F, _F, _I32, _P, _P, _P, _P, _I32,
                                        _I32, _I32, _I32, _I32, _P]),
     "moe_act_bwd_ws_bytes": (_SZ, [_I64, _I32, _I32]),
-    "moe_act_bwd": (_I32, [_P, _P, _I64, _I32, _I32, _F, _F, _P, _P, _I32, _P, _P, _I32, _P, _I32, _I32, _P, _P, _SZ, _P]),
+    "moe_act_bwd": (_I32, [_P, _I32, _P, _I64, _I32, _I32, _F, _F, _P, _P, _I32, _P, _P, _I32, _P, _I32, _I32, _P, _P, _SZ, _P]),
     "moe_adamw_plan_bytes": (_SZ, [_P, _I32]),
     "moe_adamw_plan": (_I32, [_P, _I32, _P, _SZ]),
     "moe_adamw_step": (_I32, [_P, _SZ, _P, _P, _P, ctypes.c_double, ctypes.c_double, ctypes.c_float,
@@ -552,13 +552,13 @@ def moe_act_bwd_ws_bytes(M: int, N: int, G: int) -> int:
 def moe_act_bwd(pre, dout, dpre, act, dbias=None, m_indices=None, expert_start_loc=None, num_valid=None, masked_m=None,
                 max_m=0, alpha=1.702, limit=7.0, accumulate=False, ws=None):
     """Gradient of the epilogue of moe_linear and the grouped products: dpre [M, N]
-    (may be pre) from pre [M, N] and dout [M, N or N/2], and the bias gradients
+    (may be pre) from pre [M, N] and dout [M, N or N/2] (bf16 or fp32), and the bias gradients
     dbias [G, N] ([N] or [1, N] without a layout) in bf16 or fp32, replaced or
     (accumulate) added to.  Rows: m_indices (with expert_start_loc and num_valid for
     dbias), masked_m with max_m, or all.  act "none": pre and dpre may be None.  ws:
     scratch of moe_act_bwd_ws_bytes, allocated here if not given."""
     code = _act(act)
-    _need(dout.dim() == 2, "moe_act_bwd: dout is a matrix")
+    _need(dout.dim() == 2 and dout.dtype in (_BF16, _F32), "moe_act_bwd: dout is a matrix of bf16 or fp32")
     M, cols = dout.shape
     N = 2 * cols if code >= 8 else cols
     _need(code == 0 or (pre is not None and dpre is not None), "moe_act_bwd: pre and dpre are needed")
@@ -586,8 +586,8 @@ def moe_act_bwd(pre, dout, dpre, act, dbias=None, m_indices=None, expert_start_l
         else:
             pw, nw = _dev("ws", ws.dtype, ws.shape, ws, dev), ws.numel() * ws.element_size()
     _check("moe_act_bwd", lib().moe_act_bwd(
-        None if pre is None else _dev("pre", _BF16, (M, N), pre, dev), _dev("dout", _BF16, (M, cols), dout, dev), M, N, code,
-        alpha, limit, None if m_indices is None else _dev("m_indices", _INT32, (M,), m_indices, dev),
+        None if pre is None else _dev("pre", _BF16, (M, N), pre, dev), MOE_DTYPE_FP32 if dout.dtype is _F32 else MOE_DTYPE_BF16,
+        _dev("dout", dout.dtype, (M, cols), dout, dev), M, N, code, alpha, limit, None if m_indices is None else _dev("m_indices", _INT32, (M,), m_indices, dev),
         None if masked_m is None else _dev("masked_m", _INT32, masked_m.shape, masked_m, dev), max_m, pst, pnv, G,
         None if dpre is None else _dev("dpre", _BF16, (M, N), dpre, dev), ddt, int(bool(accumulate)), pd, pw, nw,
         _raw_stream(dev)))

@@ -18,7 +18,8 @@ typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 
 struct ActBwdArgs {
   const uint16_t* pre;
-  const uint16_t* dout;
+  const void* dout;         // bf16, or (dout32) fp32
+  int dout32;
   uint16_t* dpre;
   float* part;              // [blocks][N], or null
   const int32_t* m_indices;
@@ -45,7 +46,14 @@ __device__ __forceinline__ void one_row(const ActBwdArgs& a, int64_t r, int c, f
   const int64_t wide = r * a.N + c;
   // in flight together: whether the row counts is seen when they are there
   const int tag = a.m_indices ? a.m_indices[r] : 0;
-  const u32x4 d = *reinterpret_cast<const u32x4*>(a.dout + r * a.cols + c);
+  u32x4 d, d1{};
+  if (a.dout32) {
+    const u32x4* const q = reinterpret_cast<const u32x4*>(static_cast<const float*>(a.dout) + r * a.cols + c);
+    d = q[0];
+    d1 = q[1];
+  } else {
+    d = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.dout) + r * a.cols + c);
+  }
   u32x4 g{}, u{}, og, ou;
   if (a.pre) {
     g = *reinterpret_cast<const u32x4*>(a.pre + wide);
@@ -57,7 +65,7 @@ __device__ __forceinline__ void one_row(const ActBwdArgs& a, int64_t r, int c, f
     float dg[2], du[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float da = half_of(d[i], h), x = half_of(g[i], h);
+      const float da = a.dout32 ? __uint_as_float(i < 2 ? d[2 * i + h] : d1[2 * i + h - 4]) : half_of(d[i], h), x = half_of(g[i], h);
       float v, s;
       if constexpr (GATED) {
         const float y = half_of(u[i], h);
@@ -222,8 +230,8 @@ extern "C" size_t moe_act_bwd_ws_bytes(int64_t M, int32_t N, int32_t G) {
   return (static_cast<size_t>((M + 15) / 16) + G) * N * sizeof(float);
 }
 
-extern "C" int32_t moe_act_bwd(const void* pre, const void* dout, int64_t M, int32_t N, int32_t act, float alpha,
-                               float limit, const int32_t* m_indices, const int32_t* masked_m, int32_t max_m,
+extern "C" int32_t moe_act_bwd(const void* pre, int32_t dout_dtype, const void* dout, int64_t M, int32_t N, int32_t act,
+                               float alpha, float limit, const int32_t* m_indices, const int32_t* masked_m, int32_t max_m,
                                const int32_t* expert_start_loc, const int32_t* num_valid, int32_t G, void* dpre,
                                int32_t dbias_dtype, int32_t accumulate, void* dbias, void* ws, size_t ws_bytes,
                                void* stream) {
@@ -232,6 +240,7 @@ extern "C" int32_t moe_act_bwd(const void* pre, const void* dout, int64_t M, int
   if (!make_act(act, alpha, limit, a.act)) return MOE_EINVAL;
   if (N % (a.act.gated ? 16 : 8) != 0) return MOE_EUNSUPPORTED;
   if (N > (1 << 27) || M >= (1 << 26) || G > 65535) return MOE_EUNSUPPORTED;
+  if (dout_dtype != MOE_DTYPE_BF16 && dout_dtype != MOE_DTYPE_FP32) return MOE_EUNSUPPORTED;
   if (masked_m && m_indices) return MOE_EINVAL;
   if (masked_m && (max_m <= 0 || M % max_m != 0 || (dbias && M / max_m != G))) return MOE_EINVAL;
   if (!masked_m && !m_indices && G != 1) return MOE_EINVAL;
@@ -245,7 +254,8 @@ extern "C" int32_t moe_act_bwd(const void* pre, const void* dout, int64_t M, int
   if (!aligned16(pre) || !aligned16(dout) || !aligned16(dpre) || !aligned16(dbias) || !aligned16(ws)) return MOE_EUNSUPPORTED;
   if (M == 0 && (!dbias || accumulate)) return MOE_OK;
   a.pre = a.act.kind == kActNone ? nullptr : static_cast<const uint16_t*>(pre);
-  a.dout = static_cast<const uint16_t*>(dout);
+  a.dout = dout;
+  a.dout32 = dout_dtype == MOE_DTYPE_FP32;
   a.dpre = static_cast<uint16_t*>(dpre);
   a.part = dbias ? static_cast<float*>(ws) : nullptr;
   a.m_indices = m_indices;

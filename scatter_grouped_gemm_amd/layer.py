@@ -22,6 +22,14 @@ combine, w2 (weight, then input), SiLU-and-mul, w13 (weight, then input),
 scatter -- with no further host work; optimizer() gives the AdamW step over the
 expert weights.  The gradient products end at 1,044,480 rows (8160 blocks of 128);
 a training layer with more is refused.
+
+Beside the experts: ``router=True`` gives the layer the router's own product
+(logits = x gate^T + bias in fp32, moe_linear), so that forward takes x alone;
+``shared_intermediate`` a shared expert of that width that every token goes through,
+added to the routed experts' output (its second product takes that as its
+residual); ``expert_bias`` and ``activation`` other experts than plain
+SiLU-and-mul ones (grouped_gemm_*_act).  Router and shared expert are BF16 in
+every layer.
 """
 from __future__ import annotations
 
@@ -37,7 +45,9 @@ class MoELayer:
                  fp8: bool = False, layout: str = "auto", block_e: int = 128,
                  max_m: int | None = None, expected_m: int = 0, fuse_silu: bool = True,
                  weight_format: str | None = None, train: bool = False,
-                 grad_dtype: torch.dtype = torch.bfloat16, device="cuda"):
+                 grad_dtype: torch.dtype = torch.bfloat16, device="cuda", router: bool = False,
+                 router_bias: bool = False, shared_intermediate: int = 0, expert_bias: bool = False,
+                 activation: str = "silu_mul", alpha: float = 1.702, limit: float = 7.0):
         self.H, self.I, self.E, self.k = hidden, intermediate, num_experts, top_k
         self.El = num_local_experts or num_experts
         self.expert_start = expert_start
@@ -52,6 +62,17 @@ class MoELayer:
         self.weight_format = weight_format or ("block128" if fp8 else "bf16")
         self.mx = self.weight_format in ("mxfp8", "mxfp4")
         self.wdt = self.weight_format if self.mx else fp8
+        if activation not in L.GATED_ACTIVATIONS:
+            raise ValueError(f"activation {activation!r}: one of {', '.join(L.GATED_ACTIVATIONS)}")
+        if router_bias and not router:
+            raise ValueError("router_bias without router")
+        if shared_intermediate % 128:
+            raise ValueError("shared_intermediate: a multiple of 128")
+        self.activation, self.act_args = activation, dict(alpha=alpha, limit=limit)
+        self.router, self.router_bias, self.expert_bias = router, router_bias, expert_bias
+        self.S = shared_intermediate
+        # the calls without bias and with SiLU-and-mul keep their own kernels
+        self.plain = activation == "silu_mul" and not expert_bias
         self.block_e = block_e
         self.T_max = max_tokens
         self.device = torch.device(device)
@@ -82,10 +103,14 @@ class MoELayer:
         else:
             self.rows = El * self.max_m
         R = self.rows
+        S, self.Ep = self.S, -(-self.E // 128) * 128     # Ep: the gradient products take whole 128s
         if train:        # before any memory is taken: forward alone runs with more rows
             for n, kk in ((2 * I, H), (H, I)):
                 if not L.grouped_gemm_grads_supported(R, n, kk, El):
                     raise ValueError(f"training: the gradient products do not cover {R} rows, {El} experts of {n} x {kk}")
+            for n, kk in (((2 * S, H), (H, S)) if S else ()) + (((self.Ep, H),) if router else ()):
+                if not L.grouped_gemm_grads_supported(T, n, kk, 1):
+                    raise ValueError(f"training: the gradient products do not cover {T} tokens and {n} x {kk}")
         adt = torch.uint8 if fp8 else torch.bfloat16
         # static buffers (uninitialised: every valid row is written before it is read)
         self.topk_ids = torch.empty(T, k, dtype=torch.int32, device=d)
@@ -93,7 +118,8 @@ class MoELayer:
         self.src2dst = torch.empty(T, k, dtype=torch.int32, device=d)
         self.x_buf = torch.empty(R, H, dtype=adt, device=d)
         self.x_scale = torch.empty(R * (H // 128), dtype=torch.uint8, device=d) if fp8 else None
-        self.gateup = None if fuse_silu else torch.empty(R, 2 * I, dtype=torch.bfloat16, device=d)
+        # the two halves: of SiLU-and-mul as a call of its own, and for the gradient
+        self.gateup = torch.empty(R, 2 * I, dtype=torch.bfloat16, device=d) if train or (self.plain and not fuse_silu) else None
         self.act = torch.empty(R, I, dtype=adt, device=d)
         self.act_scale = torch.empty(R * (I // 128), dtype=torch.uint8, device=d) if fp8 else None
         self.y = torch.empty(R, H, dtype=torch.bfloat16, device=d)
@@ -109,12 +135,36 @@ class MoELayer:
         ws_bytes = L.moe_scatter_ws_bytes(T, k, El, H)
         self.ws = torch.empty((ws_bytes + 3) // 4, dtype=torch.int32, device=d)
         self.w13 = self.w2 = self.w13_scale = self.w2_scale = None
+        self.b13 = self.b2 = self.gate = self.gate_bias = self.shared_w13 = self.shared_w2 = None
+        bf = lambda *shape: torch.empty(*shape, dtype=torch.bfloat16, device=d)  # noqa: E731
+        if router:
+            self.logits = torch.empty(T, self.E, dtype=torch.float32, device=d)
+        if S:
+            self.shared_act = bf(T, S)
         if train:
             self.dy = torch.empty(R, H, dtype=torch.bfloat16, device=d)
             self.dx = torch.empty(T, H, dtype=torch.bfloat16, device=d)
             self.dtopk_weights = torch.empty(T, k, dtype=torch.float32, device=d)
-            self.dlogits = torch.empty(T, self.E, dtype=torch.float32, device=d)
-        self.dw13 = self.dw2 = None
+            # with a router of its own also of the columns that fill its gradient product's 128s
+            self.dlogits = torch.empty(T, self.Ep if router else self.E, dtype=torch.float32, device=d)
+            if not self.plain:
+                self.ws_bwd = torch.empty(max(L.moe_act_bwd_ws_bytes(R, 2 * I, El), L.moe_act_bwd_ws_bytes(R, H, El), 16),
+                                          dtype=torch.uint8, device=d)
+            parts = 1 + bool(S) + bool(router)
+            if parts > 1:     # the routed, shared and router's parts of dx, each a row of a token's three
+                self.dx_parts = bf(parts * T, H)
+                token = torch.arange(T, dtype=torch.int32, device=d)
+                self.dx_maps = {n: torch.stack([token + i * T for i in range(n)], 1).contiguous() for n in range(2, parts + 1)}
+                self.one_idx = torch.zeros(T, dtype=torch.int32, device=d)     # the layout of one matrix
+                self.one_start = torch.zeros(1, dtype=torch.int32, device=d)
+                self.one_count = torch.full((1,), T, dtype=torch.int32, device=d)
+            if S:
+                self.shared_pre, self.shared_dact = bf(T, 2 * S), bf(T, S)
+            if router:
+                self.dlogits16 = bf(T, self.Ep)
+                self.ws_router = torch.empty(max(L.moe_act_bwd_ws_bytes(T, self.Ep, 1), 16), dtype=torch.uint8, device=d)
+        self.dw13 = self.dw2 = self.db13 = self.db2 = None
+        self.dgate = self.dgate_bias = self.dshared_w13 = self.dshared_w2 = None
         self._saved = None        # what the last forward left for backward
         # optional timing: name -> list of (start, end) HIP events recorded on
         # the current stream around each step of forward()
@@ -141,6 +191,45 @@ class MoELayer:
         elif self.fp8:
             self.w13_scale = torch.empty(El, 2 * I // 128, H // 128, dtype=torch.uint8, device=d)
             self.w2_scale = torch.empty(El, H // 128, I // 128, dtype=torch.uint8, device=d)
+
+    def _zeros(self, *shape, dtype=torch.bfloat16):
+        return torch.zeros(*shape, dtype=dtype, device=self.device)
+
+    def _check_extras(self):
+        """Biases, router and shared expert of this layer are there."""
+        for name, wanted, have in (("set_bias", self.expert_bias, self.b13), ("set_router", self.router, self.gate),
+                                   ("set_shared", self.S, self.shared_w13)):
+            if wanted and have is None:
+                raise ValueError(f"call {name}() first")
+
+    def set_bias(self, b13: torch.Tensor, b2: torch.Tensor):
+        """The experts' biases [El, 2I] (gate, then up) and [El, H]."""
+        if not self.expert_bias:
+            raise ValueError("the layer was made without expert_bias=True")
+        if self.b13 is None:             # in place where they are there: an optimizer may hold them
+            self.b13, self.b2 = self._zeros(self.El, 2 * self.I), self._zeros(self.El, self.H)
+        self.b13.copy_(b13)
+        self.b2.copy_(b2)
+
+    def set_router(self, gate: torch.Tensor, bias: torch.Tensor | None = None):
+        """The router's weights [E, H] and, with router_bias, its bias [E]."""
+        if not self.router or (bias is not None) != self.router_bias:
+            raise ValueError("the layer was made with another router (router=, router_bias=)")
+        if self.gate is None:            # rows past E stay zero
+            self.gate = self._zeros(self.Ep, self.H)
+            self.gate_bias = self._zeros(self.Ep, dtype=torch.float32) if self.router_bias else None
+        self.gate[:self.E].copy_(gate)
+        if bias is not None:
+            self.gate_bias[:self.E].copy_(bias)
+
+    def set_shared(self, w13: torch.Tensor, w2: torch.Tensor):
+        """The shared expert's weights [2S, H] (gate, then up) and [H, S]."""
+        if not self.S:
+            raise ValueError("the layer was made without shared_intermediate")
+        if self.shared_w13 is None:
+            self.shared_w13, self.shared_w2 = self._zeros(2 * self.S, self.H), self._zeros(self.H, self.S)
+        self.shared_w13.copy_(w13)
+        self.shared_w2.copy_(w2)
 
     def set_expert(self, e: int, w13: torch.Tensor, w2: torch.Tensor):
         """Load local expert e from bf16 weights ([2I, H] and [H, I]); FP8 layers
@@ -185,6 +274,16 @@ class MoELayer:
 
     # -- forward ----------------------------------------------------------------------
 
+    def router_logits(self, x: torch.Tensor) -> torch.Tensor:
+        """The router's logits [T, E] of x, in the layer's own buffer."""
+        if not self.router:
+            raise ValueError("the layer was made without router=True: give logits or topk_ids")
+        if self.gate is None:
+            raise ValueError("call set_router() first")
+        logits = self.logits[:x.shape[0]]
+        L.moe_linear(x, self.gate[:self.E], logits, bias=None if self.gate_bias is None else self.gate_bias[:self.E])
+        return logits
+
     def route(self, logits: torch.Tensor):
         T = logits.shape[0]
         L.moe_route_topk(logits, self.k, self.topk_ids[:T], self.topk_weights[:T])
@@ -195,6 +294,12 @@ class MoELayer:
         if T > self.T_max:
             raise ValueError(f"{T} tokens exceed the layer's static capacity {self.T_max}")
         self._saved = None       # from here on the buffers are no longer the last forward's
+        if (self.expert_bias and self.b13 is None) or (self.S and self.shared_w13 is None):
+            self._check_extras()
+        own_logits = topk_ids is None and logits is None
+        if own_logits:
+            with self._mark("router"):
+                logits = self.router_logits(x)
         if topk_ids is None:
             with self._mark("route"):
                 self.route(logits)
@@ -209,7 +314,12 @@ class MoELayer:
                 L.moe_scatter_compact(x, ids, self.expert_start, self.El, self.block_e, self.rows,
                                       fp8, self.x_buf, self.x_scale, self.m_indices,
                                       self.expert_start_loc, self.num_valid, s2d, self.ws)
-            if self.fuse_silu:
+            if not self.plain:
+                with self._mark("gemm_w13_act"):
+                    L.grouped_gemm_contig_act(wdt, self.x_buf, self.x_scale, self.w13, self.w13_scale, self.act,
+                                              self.m_indices, bias=self.b13, act=self.activation,
+                                              out_scale=self.act_scale, pre=self.gateup, **self.act_args)
+            elif self.fuse_silu:
                 with self._mark("gemm_w13_silu"):
                     L.grouped_gemm_contig_silu(wdt, self.x_buf, self.x_scale, self.w13, self.w13_scale,
                                                self.act, self.m_indices, self.act_scale)
@@ -220,14 +330,24 @@ class MoELayer:
                 with self._mark("silu_and_mul"):
                     L.silu_and_mul(self.gateup, self.act, fp8, self.act_scale, m_indices=self.m_indices)
             with self._mark("gemm_w2"):
-                L.grouped_gemm_contig(wdt, self.act, self.act_scale, self.w2, self.w2_scale, self.y,
-                                      self.m_indices)
+                if self.expert_bias:
+                    L.grouped_gemm_contig_act(wdt, self.act, self.act_scale, self.w2, self.w2_scale, self.y,
+                                              self.m_indices, bias=self.b2)
+                else:
+                    L.grouped_gemm_contig(wdt, self.act, self.act_scale, self.w2, self.w2_scale, self.y,
+                                          self.m_indices)
         else:
             El, mm = self.El, self.max_m
             with self._mark("scatter"):
                 L.moe_scatter_masked(x, ids, self.expert_start, El, mm, fp8, self.x_buf,
                                      self.x_scale, self.masked_m, s2d, self.ws)
-            if self.fuse_silu:
+            act3 = self.act.view(El, mm, I)
+            if not self.plain:
+                with self._mark("gemm_w13_act"):
+                    L.grouped_gemm_masked_act(wdt, self.x_buf.view(El, mm, self.H), self.x_scale, self.w13,
+                                              self.w13_scale, act3, self.masked_m, self.expected_m, bias=self.b13,
+                                              act=self.activation, out_scale=self.act_scale, **self.act_args)
+            elif self.fuse_silu:
                 with self._mark("gemm_w13_silu"):
                     L.grouped_gemm_masked_silu(wdt, self.x_buf.view(El, mm, self.H), self.x_scale,
                                                self.w13, self.w13_scale, self.act.view(El, mm, I),
@@ -241,14 +361,23 @@ class MoELayer:
                     L.silu_and_mul(self.gateup, self.act, fp8, self.act_scale, masked_m=self.masked_m,
                                    max_m=mm)
             with self._mark("gemm_w2"):
-                L.grouped_gemm_masked(wdt, self.act.view(El, mm, I), self.act_scale, self.w2,
-                                      self.w2_scale, self.y.view(El, mm, self.H), self.masked_m,
-                                      self.expected_m)
+                if self.expert_bias:
+                    L.grouped_gemm_masked_act(wdt, act3, self.act_scale, self.w2, self.w2_scale,
+                                              self.y.view(El, mm, self.H), self.masked_m, self.expected_m, bias=self.b2)
+                else:
+                    L.grouped_gemm_masked(wdt, act3, self.act_scale, self.w2, self.w2_scale,
+                                          self.y.view(El, mm, self.H), self.masked_m, self.expected_m)
         out = self.out[:T]
         with self._mark("combine"):
             L.moe_combine(self.y, s2d, tw, out)
+        if self.S:
+            with self._mark("shared_w13"):
+                L.moe_linear(x, self.shared_w13, self.shared_act[:T], act=self.activation,
+                             pre=self.shared_pre[:T] if self.train else None, **self.act_args)
+            with self._mark("shared_w2"):
+                L.moe_linear(self.shared_act[:T], self.shared_w2, out, residual=out)
         if self.train:
-            self._saved = (T, ids, tw, topk_ids is None)
+            self._saved = (T, ids, tw, topk_ids is None, own_logits, x if self.S or own_logits else None)
         return out
 
     __call__ = forward
@@ -256,31 +385,54 @@ class MoELayer:
     # -- training ---------------------------------------------------------------------
 
     def allocate_grads(self):
-        """The weight gradients dw13 [El, 2I, H] and dw2 [El, H, I], zero (in
-        place where the layer has them).  A captured backward needs them allocated before."""
+        """The weight gradients dw13 [El, 2I, H] and dw2 [El, H, I], and those of the
+        layer's biases (db13, db2), router (dgate [E rounded up to 128, H], dgate_bias)
+        and shared expert (dshared_w13, dshared_w2), zero (in place where the layer has
+        them).  A captured backward needs them allocated before."""
         if not self.train:
             raise ValueError("the layer was made without train=True")
         if self.dw13 is not None:        # an optimizer may hold them
-            self.dw13.zero_()
-            self.dw2.zero_()
+            for g in self.gradients():
+                g.zero_()
             return
-        self.dw13 = torch.zeros(self.El, 2 * self.I, self.H, dtype=self.grad_dtype, device=self.device)
-        self.dw2 = torch.zeros(self.El, self.H, self.I, dtype=self.grad_dtype, device=self.device)
+        zeros = lambda *shape: torch.zeros(*shape, dtype=self.grad_dtype, device=self.device)  # noqa: E731
+        H, I, S = self.H, self.I, self.S
+        self.dw13, self.dw2 = zeros(self.El, 2 * I, H), zeros(self.El, H, I)
+        if self.expert_bias:
+            self.db13, self.db2 = zeros(self.El, 2 * I), zeros(self.El, H)
+        if self.router:
+            self.dgate = zeros(self.Ep, H)
+            self.dgate_bias = torch.zeros(self.Ep, dtype=torch.float32, device=self.device) if self.router_bias else None
+        if S:
+            self.dshared_w13, self.dshared_w2 = zeros(2 * S, H), zeros(H, S)
+
+    def _of(self, *names):
+        return [t for t in (getattr(self, n) for n in names) if t is not None]
+
+    def parameters(self):
+        """The layer's weights, in the order of gradients()."""
+        return self._of("w13", "w2", "b13", "b2", "gate", "gate_bias", "shared_w13", "shared_w2")
+
+    def gradients(self):
+        return self._of("dw13", "dw2", "db13", "db2", "dgate", "dgate_bias", "dshared_w13", "dshared_w2")
 
     def backward(self, dout: torch.Tensor, *, accumulate: bool = False):
-        """Gradients of the last forward: writes (or, accumulate, adds to) dw13 and
-        dw2 and returns (dx [T, H], dlogits [T, E]), or (dx, dtopk_weights [T, k])
-        where forward was given topk_ids.  The results are the layer's own buffers.
+        """Gradients of the last forward: writes (or, accumulate, adds to) the layer's
+        weight gradients and returns (dx [T, H], dlogits [T, E]), or (dx, dtopk_weights
+        [T, k]) where forward was given topk_ids.  The results are the layer's own
+        buffers (dlogits of the layer's own router a slice of wider rows).  Where forward
+        was given logits or ids, the router's gradients are left as they are.
 
         With a share of the experts, dx and dlogits are that share's part: both
         add up over the shares.  What forward kept is used up: one backward for
-        each forward that came to its end, and ids and weights given to forward
-        must still be as they were."""
+        each forward that came to its end, and ids and weights given to forward (with
+        a router or a shared expert x too) must still be as they were.  With a share of
+        the experts the shared expert and the router's bias belong to one share alone."""
         if not self.train:
             raise ValueError("the layer was made without train=True")
         if self._saved is None:
             raise ValueError("backward needs a forward of its own before it")
-        T, ids, tw, routed = self._saved
+        T, ids, tw, routed, own_logits, x = self._saved
         if dout.shape != (T, self.H):
             raise ValueError(f"dout: want {(T, self.H)}, got {tuple(dout.shape)}")
         if self.dw13 is None:
@@ -289,37 +441,84 @@ class MoELayer:
                 raise ValueError("call allocate_grads() before backward is captured")
             self.allocate_grads()
         s2d, dx, dtw = self.src2dst[:T], self.dx[:T], self.dtopk_weights[:T]
+        dlogits = self.dlogits[:T]
+        if routed and not own_logits and self.router:      # rows of E, as the caller's logits
+            dlogits = self.dlogits.view(-1)[:T * self.E].view(T, self.E)
         m_idx, starts, counts = self.m_indices, self.expert_start_loc, self.num_valid
         with self._mark("combine_bwd"):
             L.moe_combine_bwd(dout, self.y, s2d, tw, self.dy, dtw)
         self._saved = None
         if routed:
             with self._mark("route_bwd"):
-                L.moe_route_topk_bwd(ids, tw, dtw, self.dlogits[:T])
+                L.moe_route_topk_bwd(ids, tw, dtw, dlogits)
+        if self.expert_bias:
+            with self._mark("bias_bwd_w2"):
+                L.moe_act_bwd(None, self.dy, None, "none", dbias=self.db2, m_indices=m_idx, expert_start_loc=starts,
+                              num_valid=counts, accumulate=accumulate, ws=self.ws_bwd)
         with self._mark("wgrad_w2"):
             L.grouped_gemm_contig_wgrad(self.dy, self.act, starts, counts, self.dw2, accumulate)
         dact = self.act          # the activation has been used: its buffer takes the gradient
         with self._mark("dgrad_w2"):
             L.grouped_gemm_contig_dgrad(self.dy, self.w2, dact, m_idx)
-        with self._mark("silu_bwd"):
-            L.silu_and_mul_bwd(self.gateup, dact, self.gateup, m_indices=m_idx)
+        if self.plain:
+            with self._mark("silu_bwd"):
+                L.silu_and_mul_bwd(self.gateup, dact, self.gateup, m_indices=m_idx)
+        else:
+            with self._mark("act_bwd"):
+                L.moe_act_bwd(self.gateup, dact, self.gateup, self.activation, dbias=self.db13, m_indices=m_idx,
+                              expert_start_loc=starts, num_valid=counts, accumulate=accumulate, ws=self.ws_bwd,
+                              **self.act_args)
         with self._mark("wgrad_w13"):
             L.grouped_gemm_contig_wgrad(self.gateup, self.x_buf, starts, counts, self.dw13, accumulate)
         with self._mark("dgrad_w13"):
             L.grouped_gemm_contig_dgrad(self.gateup, self.w13, self.y, m_idx)
+        parts = [dx] if not (self.S or own_logits) else list(self.dx_parts.view(-1, self.T_max, self.H)[:, :T])
         with self._mark("scatter_bwd"):
-            L.moe_scatter_bwd(self.y, s2d, dx)
-        return dx, (self.dlogits[:T] if routed else dtw)
+            L.moe_scatter_bwd(self.y, s2d, parts[0])
+        if self.S:
+            self._shared_bwd(dout, x, parts[1], accumulate)
+        if own_logits:
+            self._router_bwd(dlogits, x, parts[1 + bool(self.S)], accumulate)
+        if len(parts) > 1:
+            with self._mark("dx_sum"):
+                L.moe_scatter_bwd(self.dx_parts, self.dx_maps[1 + bool(self.S) + bool(own_logits)][:T], dx)
+        return dx, (dlogits[:, :self.E] if routed else dtw)
+
+    def _one_matrix_bwd(self, dc, x, w, dw, dx, accumulate):
+        """Gradients of one matrix w [N, K]: the grouped products with one expert."""
+        T = dc.shape[0]
+        L.grouped_gemm_contig_wgrad(dc, x, self.one_start, self.one_count, dw[None], accumulate)
+        L.grouped_gemm_contig_dgrad(dc, w[None], dx, self.one_idx[:T])
+
+    def _shared_bwd(self, dout, x, dx, accumulate):
+        T = dout.shape[0]
+        dact, pre = self.shared_dact[:T], self.shared_pre[:T]
+        with self._mark("shared_w2_bwd"):
+            self._one_matrix_bwd(dout, self.shared_act[:T], self.shared_w2, self.dshared_w2, dact, accumulate)
+        with self._mark("shared_act_bwd"):
+            L.moe_act_bwd(pre, dact, pre, self.activation, **self.act_args)
+        with self._mark("shared_w13_bwd"):
+            self._one_matrix_bwd(pre, x, self.shared_w13, self.dshared_w13, dx, accumulate)
+
+    def _router_bwd(self, dlogits, x, dx, accumulate):
+        """The logits' gradient is rounded to bf16 for the products, as every gradient here is;
+        the bias takes it in fp32."""
+        T = dlogits.shape[0]
+        d16 = self.dlogits16[:T]
+        with self._mark("router_bwd"):
+            L.moe_act_bwd(None, dlogits, d16, "none", dbias=self.dgate_bias, accumulate=accumulate, ws=self.ws_router)
+            self._one_matrix_bwd(d16, x, self.gate, self.dgate, dx, accumulate)
 
     def optimizer(self, **kw) -> AdamW:
-        """AdamW (optim.AdamW's arguments) over the expert weights and their gradients."""
+        """AdamW (optim.AdamW's arguments) over the layer's weights and their gradients."""
         if not self.train:
             raise ValueError("the layer was made without train=True")
         if self.w13 is None:
             raise ValueError("set the weights first: the masters are taken from them")
         if self.dw13 is None:
             self.allocate_grads()
-        return AdamW([self.w13, self.w2], [self.dw13, self.dw2], **kw)
+        self._check_extras()
+        return AdamW(self.parameters(), self.gradients(), **kw)
 
 
 class _NoMark:

@@ -71,8 +71,8 @@ def test_grouped_refusals_of_one_layout():
 
 
 def bwd(pre=P, dout=P, M=2560, N=256, act=9, alpha=1.702, limit=7.0, m=None, mm=None, max_m=0, st=None, nv=None, G=1,
-        dpre=P, ddt=16, acc=0, db=None, ws=P, nws=1 << 30):
-    return L.lib().moe_act_bwd(pre, dout, M, N, act, alpha, limit, m, mm, max_m, st, nv, G, dpre, ddt, acc, db, ws, nws, None)
+        dpre=P, ddt=16, acc=0, db=None, ws=P, nws=1 << 30, odt=0):
+    return L.lib().moe_act_bwd(pre, odt, dout, M, N, act, alpha, limit, m, mm, max_m, st, nv, G, dpre, ddt, acc, db, ws, nws, None)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -81,7 +81,7 @@ def bwd(pre=P, dout=P, M=2560, N=256, act=9, alpha=1.702, limit=7.0, m=None, mm=
     (dict(act=0, dpre=None), L.MOE_EINVAL), (dict(m=P, mm=P, max_m=64), L.MOE_EINVAL), (dict(mm=P), L.MOE_EINVAL),
     (dict(mm=P, max_m=100), L.MOE_EINVAL), (dict(mm=P, max_m=64, G=3, db=P), L.MOE_EINVAL), (dict(G=2), L.MOE_EINVAL),
     (dict(m=P, db=P, G=2), L.MOE_EINVAL), (dict(m=P, db=P, G=2, st=P), L.MOE_EINVAL), (dict(db=P, ws=None), L.MOE_EINVAL),
-    (dict(db=P, nws=16), L.MOE_ECAPACITY), (dict(db=P, ddt=1), L.MOE_EUNSUPPORTED), (dict(N=8), L.MOE_EUNSUPPORTED),
+    (dict(db=P, nws=16), L.MOE_ECAPACITY), (dict(db=P, ddt=1), L.MOE_EUNSUPPORTED), (dict(odt=1), L.MOE_EUNSUPPORTED), (dict(N=8), L.MOE_EUNSUPPORTED),
     (dict(act=1, N=4), L.MOE_EUNSUPPORTED), (dict(M=1 << 26), L.MOE_EUNSUPPORTED), (dict(N=(1 << 27) + 16), L.MOE_EUNSUPPORTED),
     (dict(pre=BAD), L.MOE_EUNSUPPORTED), (dict(dout=BAD), L.MOE_EUNSUPPORTED), (dict(dpre=BAD), L.MOE_EUNSUPPORTED),
     (dict(db=BAD), L.MOE_EUNSUPPORTED), (dict(db=P, ws=BAD), L.MOE_EUNSUPPORTED), (dict(M=0, pre=None, dout=None), L.MOE_OK),

@@ -439,6 +439,20 @@ def test_act_bwd(act, layout, db, acc):
             check(dbias[g], s, bound + HALF[db] * (s.abs() + bound), ("dbias", g))
 
 
+@pytest.mark.parametrize("act", ["none", "gelu", "swiglu_clamp"])
+@pytest.mark.parametrize("M,N", [(5, 16), (300, 272), (1500, 1024)])
+def test_act_bwd_of_an_fp32_output(act, M, N):
+    """dout in fp32, as moe_linear's fp32 output has it; act none rounds it to bf16."""
+    announce("fp32 dout", act, M, N)
+    wide = N // 2 if act in GATED else N
+    pre, dout = rand(1, M, N, scale=3.0), rand(2, M, wide, dtype=F32)
+    dpre, db = torch.empty(M, N, dtype=BF, device=DEV), torch.empty(N, dtype=F32, device=DEV)
+    L.moe_act_bwd(None if act == "none" else pre, dout, dpre, act, dbias=db, alpha=ALPHA, limit=LIMIT)
+    want, t = exact_bwd(pre.double(), dout.double(), act), 2.0 ** -20 * bwd_terms(pre.double(), dout.double(), act)
+    check(dpre, want, t + HALF[BF] * (want.abs() + t), "dpre")
+    check(db, want.sum(0), t.sum(0) + (M + 4) * 2.0 ** -24 * (want.abs() + t).sum(0) + HALF[F32] * want.sum(0).abs(), "dbias")
+
+
 def test_bias_gradient_alone():
     d = rand(1, 1000, 264)
     db = torch.empty(264, dtype=F32, device=DEV)

@@ -29,6 +29,18 @@
 //   - The bias of a wavefront's 64 columns goes to LDS behind the stores of the tile
 //     before, a load that the waits count like those stores.
 //
+// Measured (us; in brackets TFLOP/s; one matrix, torch's bf16 library product in turn, which
+// has no epilogue):
+//   4096 x 4096 x 28672 650 (1480), gated with pre 690; library 624 (1541).  8192 cubed 716
+//   (1534); 666 (1651).  16384 x 1536 x 4096 154 (1340), residual 178; 150 (1377).  8191 x
+//   2048 x 7168 188 (1278), residual 208; 174 (1385).  8000 x 4104 x 8200 469 (1148; K and N
+//   with part steps and columns)
+//   8 experts of 1024 rows, 28672 x 4096 gated with pre 1580 (1220); 128 ragged ones, 4096
+//   x 1536, 131072 rows 1540 (1070)
+// What bounds it: within a tile the card's power (matrix cores busy 80% of the cycles at
+// 1.64 GHz; 1.33 us a step, 1620 TFLOP/s); between tiles 6 to 8 us, of which 2 to 5 are all
+// CUs' stores at the same time and 3 the arithmetic of the epilogue.  No LDS bank conflicts.
+//
 // Sums run through v_mfma_f32_16x16x32_bf16 in the order of the other kernels of these
 // products (linear.hip, gemm_kernel.h), so a row has the same bits from each.
 #include <mutex>
@@ -74,7 +86,9 @@ __device__ __forceinline__ u32x4 pack8_add(f32x4 v0, f32x4 v1, u32x4 r) {
 
 // GROUPED: the compact layout; else one matrix, whose tiles are whole but for one row of
 // them, so that leaving out a half would cost more (a branch a phase, 1%) than it gains.
-template <bool GROUPED, bool GATED, bool PRE, bool RES>
+// TAIL: K is no multiple of 64.  What a row's last step holds behind K is read as 0 by
+// both operands: the lanes that carry it get an offset outside the buffer.
+template <bool GROUPED, bool GATED, bool PRE, bool RES, bool TAIL>
 __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   static_assert(!RES || !(GROUPED || GATED || PRE), "no store for gated ones; too many registers with pre");
@@ -132,7 +146,7 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
     t.nt = r.nt;
     return true;
   };
-  const int real = a.K / kStep;            // steps that hold something
+  const int real = TAIL ? (a.K + kStep - 1) / kStep : a.K / kStep;  // steps that hold something
   const int steps = (real + 1) / 2 * 2;    // a tile is a whole number of pairs of steps
   Tile lt;  // load side
   if (!fetch(lt)) return;
@@ -155,6 +169,12 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
     if constexpr (GATED) r = (r >> 6) * 32 + (r & 31) + ((r >> 5) & 1) * a.cols;
     vq[j] = static_cast<uint32_t>(r * ldb) + chunk[j & 1];
   }
+  // lanes whose 16 bytes are in the step, of even and of odd loads
+  [[maybe_unused]] uint64_t keep[2] = {~0ull, ~0ull};
+  [[maybe_unused]] uint64_t last[2];
+  if constexpr (TAIL)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) last[j] = __ballot(static_cast<int>(chunk[j]) < (a.K - (real - 1) * kStep) * 2);
   const uint8_t *bp, *bq;  // this step's operands
   int np, np1;             // bytes within bounds of A's halves
   uint32_t nq;
@@ -169,21 +189,26 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
     int nr = GATED ? a.cols + kCols : kCols;  // B rows that the tile's offsets reach
     nr = nr < N - n0 ? nr : N - n0;
     nq = static_cast<uint32_t>(nr * lq);
+    if constexpr (TAIL) keep[0] = keep[1] = ~0ull;  // a tile has two steps at least
   };
   lset();
   // No immediate offset in these loads: the instruction adds it to the LDS address too.
   auto to_lds = [&](__amdgpu_buffer_rsrc_t rs, uint8_t* dst, uint32_t off) __attribute__((always_inline)) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16, off, 0, 0, 0);
   };
+  auto kept = [&](uint32_t off, int j) __attribute__((always_inline)) -> uint32_t {
+    if constexpr (TAIL) return __builtin_amdgcn_inverse_ballot_w64(keep[j & 1]) ? off : 0xfffffff0u;
+    return off;
+  };
   auto load_p = [&](uint8_t* dst, int half) __attribute__((always_inline)) {
     const auto rs = !half ? buffer(bp, np) : buffer(bp + 128 * a.lda, np1);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) to_lds(rs, dst + (wave * 2 + j) * 1024, vp[j]);
+    for (int j = 0; j < 2; ++j) to_lds(rs, dst + (wave * 2 + j) * 1024, kept(vp[j], j));
   };
   auto load_q = [&](uint8_t* dst) __attribute__((always_inline)) {
     const auto rs = buffer_u(bq, nq);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) to_lds(rs, dst + (wave * 4 + j) * 1024, vq[j]);
+    for (int j = 0; j < 4; ++j) to_lds(rs, dst + (wave * 4 + j) * 1024, kept(vq[j], j));
   };
   // on to the next step; behind the last tile its last step is read again (and never
   // used), so that every step issues the same loads.  The step that makes an odd
@@ -206,6 +231,11 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
     } else {
       bp += kStep * 2;
       bq += kStep * 2;
+      if constexpr (TAIL)
+        if (lk == real - 1) {
+          keep[0] = last[0];
+          keep[1] = last[1];
+        }
     }
   };
 
@@ -315,7 +345,9 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
     // of a lane's 16 bytes in a half's 64: a store covers 16 rows.  (Whole lines of eight
     // rows take an exchange between lanes, which costs more than the stores gain: 4096 x
     // 1536, 16384 rows, us 162 and 160, with GELU 202 and 198.)
-    const uint32_t o32 = ((g & 1) * 16 + (g >> 1) * 8) * 2;
+    const int lc = (g & 1) * 16 + (g >> 1) * 8;
+    // columns behind the last one: outside every buffer here (below 2^31 bytes)
+    const uint32_t o32[2] = {c0 + lc < cols ? lc * 2u : 0x80000000u, c0 + lc + 32 < cols ? lc * 2u + 64 : 0x80000000u};
     // the lines of the quadrants' 64 rows from column col on
     const auto part = [&](const void* p, int64_t line, int hp, int col) __attribute__((always_inline)) {
       const int r0 = hp * 128 + wm * 64;
@@ -335,7 +367,7 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            old[hp][i][h] = __builtin_amdgcn_raw_buffer_load_b128(rr, (i * 16 + row) * rline + o32 + h * 64, 0, 0);
+            old[hp][i][h] = __builtin_amdgcn_raw_buffer_load_b128(rr, (i * 16 + row) * rline + o32[h], 0, 0);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -346,7 +378,7 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
           const auto rg = part(a.pre, pline, hp, c0), ru = part(a.pre, pline, hp, c0 + cols);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t off = (i * 16 + row) * pline + o32;
+            const uint32_t off = (i * 16 + row) * pline + o32[0];
             __builtin_amdgcn_raw_buffer_store_b128(pack8(acc[hp][0][i][0], acc[hp][0][i][1]), rg, off, 0, 0);
             __builtin_amdgcn_raw_buffer_store_b128(pack8(acc[hp][1][i][0], acc[hp][1][i][1]), ru, off, 0, 0);
           }
@@ -357,7 +389,7 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
           f32x4 v[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) v[j] = act::gated4(a.act, acc[hp][0][i][j], acc[hp][1][i][j]);
-          __builtin_amdgcn_raw_buffer_store_b128(pack8(v[0], v[1]), rd, (i * 16 + row) * oline + o32, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b128(pack8(v[0], v[1]), rd, (i * 16 + row) * oline + o32[0], 0, 0);
         }
       } else {
         if constexpr (PRE) {
@@ -369,7 +401,7 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
             for (int hq = 0; hq < 2; ++hq) w[hq] = pack8(acc[hp][hq][i][0], acc[hp][hq][i][1]);
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              __builtin_amdgcn_raw_buffer_store_b128(w[h], rd, (i * 16 + row) * pline + o32 + h * 64, 0, 0);
+              __builtin_amdgcn_raw_buffer_store_b128(w[h], rd, (i * 16 + row) * pline + o32[h], 0, 0);
           }
         }
         const auto rd = part(a.out, oline, hp, c0);
@@ -383,7 +415,7 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            __builtin_amdgcn_raw_buffer_store_b128(w[h], rd, (i * 16 + row) * oline + o32 + h * 64, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(w[h], rd, (i * 16 + row) * oline + o32[h], 0, 0);
         }
       }
     }
@@ -480,7 +512,12 @@ template <bool GROUPED, bool GATED, bool PRE, bool RES = false>
 int32_t launch(const LinearArgs& a, hipStream_t s) {
   const int grid = linear_cus();  // one workgroup per CU
   if (grid == 0) return MOE_EDEVICE;
-  linear_wide_kernel<GROUPED, GATED, PRE, RES><<<grid, kThreads, 0, s>>>(a);
+  if constexpr (GROUPED)
+    linear_wide_kernel<GROUPED, GATED, PRE, RES, false><<<grid, kThreads, 0, s>>>(a);
+  else if (a.K % kStep == 0)
+    linear_wide_kernel<GROUPED, GATED, PRE, RES, false><<<grid, kThreads, 0, s>>>(a);
+  else
+    linear_wide_kernel<GROUPED, GATED, PRE, RES, true><<<grid, kThreads, 0, s>>>(a);
   MOE_CHECK_LAUNCH();
   return MOE_OK;
 }
@@ -503,7 +540,7 @@ int linear_cus() {
 
 bool linear_wide_covers(const LinearArgs& a) {
   const int64_t ldb = static_cast<int64_t>(a.K) * 2;
-  return !a.out32 && a.vec8 && !(a.residual && (a.m_indices || a.act.gated || a.pre)) && a.K % kStep == 0 && a.K >= 2 * kStep && a.cols % 64 == 0 &&
+  return !a.out32 && a.vec8 && !(a.residual && (a.m_indices || a.act.gated || a.pre)) && (!a.m_indices || a.K % kStep == 0) && a.K > kStep &&
          // 32-bit offsets: 256 rows of A, out and pre, of B 256 rows or (gated) half of all
          a.lda <= (1 << 22) && a.ldo <= (1 << 21) && a.ldr <= (1 << 21) && a.N <= (1 << 21) &&
          (a.act.gated ? (static_cast<int64_t>(a.cols) + 256) * ldb < (1ll << 32) : a.K <= (1 << 21)) &&

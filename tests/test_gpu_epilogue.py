@@ -76,6 +76,40 @@ def test_linear_large(T, K, N, act, residual, pre):
     run_linear(T, K, N, act, BF, residual, BF, pre, seed=T)
 
 
+@pytest.mark.parametrize("T,K,N,act,residual,pre,pad", [
+    (4100, 1032, 4104, "none", False, False, 0), (4099, 200, 4520, "gelu", True, False, 8), (2050, 328, 10016, "silu_mul", False, True, 0),
+    (2309, 1096, 6416, "swiglu_clamp", False, False, 200), (3001, 72, 5192, "relu2", False, True, 0), (6000, 136, 2056, "none", True, False, 0),
+    (2560, 704, 4168, "none", True, False, 0), (2600, 1000, 8208, "gelu_tanh_mul", False, True, 0)])
+def test_linear_large_and_odd(T, K, N, act, residual, pre, pad):
+    """Large tiles whose last step and last columns are part ones."""
+    run_linear(T, K, N, act, BF, residual, BF, pre, pad, seed=T)
+
+
+@pytest.mark.parametrize("K,N", [(1000, 4360), (456, 5000)])
+def test_linear_odd_rows_do_not_depend_on_each_other(K, N):
+    w, x = rand(1, N, K, scale=K ** -0.5), rand(3, 4000, K)
+    for act in ("none", "gelu_mul"):
+        wide = N // 2 if act in GATED else N
+        whole = torch.empty(4000, wide, dtype=BF, device=DEV)
+        L.moe_linear(x, w, whole, act=act)
+        for a, n in [(0, 1), (3999, 1), (100, 33), (1000, 130), (2000, 600), (0, 1500)]:
+            o = torch.empty(n, wide, dtype=BF, device=DEV)
+            L.moe_linear(x[a:a + n], w, o, act=act)
+            assert torch.equal(o, whole[a:a + n]), (act, a, n)
+
+
+def test_linear_rows_with_nan_behind_k():
+    """What lies behind a row's K columns, in the gap to the next row, is never part of a sum."""
+    for T, K, N in [(3, 72, 64), (200, 72, 256), (4000, 200, 4104), (4000, 712, 4104)]:
+        wide = torch.full((T, K + 56), float("nan"), dtype=BF, device=DEV)
+        wide[:, :K] = rand(1, T, K)
+        w = rand(2, N, K, scale=K ** -0.5)
+        o, ref = torch.empty(T, N, dtype=BF, device=DEV), torch.empty(T, N, dtype=BF, device=DEV)
+        L.moe_linear(wide[:, :K], w, o)
+        L.moe_linear(wide[:, :K].contiguous(), w, ref)
+        assert torch.equal(o, ref) and not torch.isnan(o).any(), (T, K, N)
+
+
 def test_linear_rows_do_not_depend_on_each_other():
     """A row has the same bits whatever the number of rows, so from every kernel that the sizes choose."""
     K, N = 1152, 2560

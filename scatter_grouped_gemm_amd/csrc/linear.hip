@@ -11,7 +11,7 @@
 //     and B; chunks are permuted within a row so that the 16 lanes of a fragment
 //     read hit different banks.  The next step's fragments are read while a step's MFMAs
 //     run.  What bounds a tile by itself is LDS: a 64 x 64 step (0.29 us) reads 32 KB
-//     from it and writes 16; deeper stages change nothing.
+//     from it and writes 16.
 //   - The order of the tiles keeps those that share rows on one XCD: 8192 rows, K 7168, N
 //     256 46 us, dealt over all of them 68 (each L2 then reads A).
 //   - Whatever lies outside (rows behind the last, k behind K) is read as 0 through
@@ -28,16 +28,17 @@ namespace {
 constexpr uint32_t kOutside = 0xfffffff0u;  // beyond any descriptor here
 
 template <int BM, int BN, int S, bool GATED>
-__global__ __launch_bounds__(256, 2) void linear_tile_kernel(const LinearArgs a) {
+__global__ __launch_bounds__(256, S > 4 ? 1 : 2) void linear_tile_kernel(const LinearArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int WM = BM / 2, WN = BN / 2, TM = WM / 16, TN = WN / 16;
   constexpr int LA = BM / 32, LB = BN / 32;  // 1 KB loads of a wavefront and step
   constexpr int NC = GATED ? BN / 2 : BN;    // output columns of a tile
   constexpr int STAGE = (BM + BN) * 128;
   static_assert(LA % 2 == 0 && LB % 2 == 0, "whole pairs of loads");
-  static_assert((S == 2 || S == 4) && (LA + LB) * (S - 2) < 64, "loads in flight");
+  static_assert((S == 2 || S == 4 || S == 6) && (LA + LB) * (S - 2) < 64, "loads in flight");
   // Arrays of their own: the compiler then knows which loads to LDS a read can depend on.
-  __shared__ __attribute__((aligned(1024))) uint8_t s0[STAGE], s1[STAGE], s2[S > 2 ? STAGE : 1], s3[S > 2 ? STAGE : 1];
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[STAGE], s1[STAGE], s2[S > 2 ? STAGE : 1], s3[S > 2 ? STAGE : 1],
+      s4[S > 4 ? STAGE : 1], s5[S > 4 ? STAGE : 1];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
@@ -159,6 +160,10 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(const LinearArgs a)
     load(s2);
     load(s3);
   }
+  if constexpr (S > 4) {
+    load(s4);
+    load(s5);
+  }
   fence();
   wait_vm<(LA + LB) * (S - 1)>();
   barrier();
@@ -171,7 +176,13 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(const LinearArgs a)
     if constexpr (S > 2) {
       step(f0, f1, s2, s3);
       if (++t >= steps) break;
-      step(f1, f0, s3, s0);
+      step(f1, f0, s3, S > 4 ? s4 : s0);
+      if (++t >= steps) break;
+    }
+    if constexpr (S > 4) {
+      step(f0, f1, s4, s5);
+      if (++t >= steps) break;
+      step(f1, f0, s5, s0);
       if (++t >= steps) break;
     }
   }
@@ -233,7 +244,8 @@ void linear_alignment(LinearArgs& a) {
 //   128 x 128 for three tiles for two CUs and up, two workgroups a CU: 448 tiles 62 (128 x
 //     64 92, 64 x 64 87)
 //   64 x 64 up to two tiles a CU: 64 tiles* 33 (128 x 64 49, 128 x 128 73), 512 tiles* (N
-//     256) 46 (53, 78)
+//     256) 46 (53, 78); with one tile a CU in six stages, for operands that come from HBM:
+//     256 tiles* 45 (four stages 48), 512 tiles* 88 (70)
 //   128 x 64 between them: 512 tiles* 75 (128 x 128 76, 64 x 64 88)
 int32_t launch_linear(const LinearArgs& a, hipStream_t s) {
   const int64_t cus = linear_cus(), n = a.N;
@@ -241,7 +253,9 @@ int32_t launch_linear(const LinearArgs& a, hipStream_t s) {
   if (!a.m_indices && a.M <= 32 && n <= 16384) return launch_linear_thin(a, s);
   if (linear_wide_covers(a) && 2 * ((a.M + 255) / 256 * ((n + 255) / 256)) > cus) return launch_linear_wide(a, s);
   if (2 * ((a.M + 127) / 128 * ((n + 127) / 128)) >= 3 * cus) return launch<128, 128, 2>(a, s);
-  if ((a.M + 63) / 64 * ((n + 63) / 64) <= 2 * cus) return launch<64, 64, 4>(a, s);
+  const int64_t small = (a.M + 63) / 64 * ((n + 63) / 64);
+  if (small <= cus) return launch<64, 64, 6>(a, s);
+  if (small <= 2 * cus) return launch<64, 64, 4>(a, s);
   return launch<128, 64, 2>(a, s);
 }
 

@@ -64,7 +64,7 @@ def _no_spills(found, text, n):
 def test_no_register_is_spilled(wide, thin, tile):
     _no_spills(*wide, 14)    # (grouped, gated, pre, residual, tail)
     _no_spills(*thin, 12)    # (loads of A, blocks of 16 rows of B, gated)
-    _no_spills(*tile, 6)     # (BM, BN, stages, gated)
+    _no_spills(*tile, 8)     # (BM, BN, stages, gated)
 
 
 def _to_lds(line, width="dwordx4"):

@@ -428,6 +428,7 @@ int32_t moe_combine(const void* Y, int64_t num_rows, const int32_t* src2dst,
  *   out          device, out_dtype MOE_DTYPE_BF16 or MOE_DTYPE_FP32, row m at
  *                out + m*ld_out
  *   pre          device bf16 [M][N], out: p for moe_act_bwd, or NULL
+ * out and pre hold no element of A, B, bias or each other.
  * Limits: K % 8 == 0, lda % 8 == 0 and >= K, A and B 16-byte aligned, ld_out and
  * ld_residual at least the output's columns, N even with a gated activation, and then
  * (N/2 + 256) * K * 2 < 2^32; lda < 2^22, M < 2^31, ceil(M / 128) * ceil(N / 128) < 2^24. */

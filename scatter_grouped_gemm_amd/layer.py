@@ -29,7 +29,8 @@ Beside the experts: ``router=True`` gives the layer the router's own product
 added to the routed experts' output (its second product takes that as its
 residual); ``expert_bias`` and ``activation`` other experts than plain
 SiLU-and-mul ones (grouped_gemm_*_act).  Router and shared expert are BF16 in
-every layer.
+every layer.  Where the experts are shared out over several layers, one of them has
+the shared expert, since their outputs are added up.
 """
 from __future__ import annotations
 

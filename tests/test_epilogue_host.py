@@ -12,7 +12,7 @@ BAD = 4104      # not 16-byte aligned
 INF = float("inf")
 
 
-def linear(A=P, lda=256, B=P, bias=None, bdt=0, act=0, alpha=1.702, limit=7.0, res=None, ldr=0, odt=0, out=P, ldo=64,
+def linear(A=P, lda=256, B=2 * P, bias=None, bdt=0, act=0, alpha=1.702, limit=7.0, res=None, ldr=0, odt=0, out=3 * P, ldo=64,
            pre=None, M=4, N=64, K=256):
     return L.lib().moe_linear(A, lda, B, bias, bdt, act, alpha, limit, res, ldr, odt, out, ldo, pre, M, N, K, None)
 
@@ -30,18 +30,20 @@ def linear(A=P, lda=256, B=P, bias=None, bdt=0, act=0, alpha=1.702, limit=7.0, r
     (dict(pre=4097), L.MOE_EUNSUPPORTED), (dict(lda=1 << 22), L.MOE_EUNSUPPORTED),
     (dict(act=9, N=1 << 20, K=4096, lda=4096, ldo=1 << 20), L.MOE_EUNSUPPORTED),
     (dict(M=(1 << 30), N=1 << 20, ldo=1 << 20), L.MOE_EUNSUPPORTED),
+    (dict(out=P), L.MOE_EINVAL), (dict(out=2 * P), L.MOE_EINVAL), (dict(pre=P), L.MOE_EINVAL), (dict(pre=3 * P), L.MOE_EINVAL),
+    (dict(res=3 * P, ldr=72), L.MOE_EINVAL),              # in place, but with other rows
     (dict(M=0, A=None, B=None, out=None), L.MOE_OK),
 ])
 def test_linear_refusals(kw, want):
     assert linear(**kw) == want
 
 
-def contig(dtype=0, A=P, As=None, B=P, Bs=None, bias=None, bdt=0, act=0, alpha=1.702, limit=7.0, odt=0, out=P, os=None,
+def contig(dtype=0, A=P, As=None, B=2 * P, Bs=None, bias=None, bdt=0, act=0, alpha=1.702, limit=7.0, odt=0, out=3 * P, os=None,
            pre=None, m=P, M=256, N=256, K=256, G=2):
     return L.lib().grouped_gemm_contig_act(dtype, A, As, B, Bs, bias, bdt, act, alpha, limit, odt, out, os, pre, m, M, N, K, G, None)
 
 
-def masked(dtype=0, A=P, As=None, B=P, Bs=None, bias=None, bdt=0, act=0, alpha=1.702, limit=7.0, odt=0, out=P, os=None,
+def masked(dtype=0, A=P, As=None, B=2 * P, Bs=None, bias=None, bdt=0, act=0, alpha=1.702, limit=7.0, odt=0, out=3 * P, os=None,
            pre=None, m=P, em=0, max_m=64, N=256, K=256, G=2):
     return L.lib().grouped_gemm_masked_act(dtype, A, As, B, Bs, bias, bdt, act, alpha, limit, odt, out, os, pre, m, em, max_m, N, K, G, None)
 
@@ -58,7 +60,7 @@ def masked(dtype=0, A=P, As=None, B=P, Bs=None, bias=None, bdt=0, act=0, alpha=1
     (dict(dtype=1, As=P, Bs=P, pre=P), L.MOE_EUNSUPPORTED),                             # pre needs bf16 weights
     (dict(A=BAD), L.MOE_EUNSUPPORTED), (dict(B=BAD), L.MOE_EUNSUPPORTED), (dict(bias=BAD), L.MOE_EUNSUPPORTED),
     (dict(out=BAD), L.MOE_EUNSUPPORTED), (dict(pre=BAD), L.MOE_EUNSUPPORTED),
-    (dict(act=9, N=1 << 20, K=4096), L.MOE_EUNSUPPORTED),
+    (dict(act=9, N=1 << 20, K=4096), L.MOE_EUNSUPPORTED), (dict(out=P), L.MOE_EINVAL), (dict(pre=3 * P), L.MOE_EINVAL),
 ])
 def test_grouped_refusals(call, kw, want):
     assert call(**kw) == want

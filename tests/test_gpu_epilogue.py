@@ -259,6 +259,7 @@ def grouped_inputs(counts, K, N, fmt, act, bias, layout, max_m=0, seed=0):
         return x, w, b, m, idx, m[idx].long()
     x = rand(seed, G, max_m, K)
     c = i32_dev(np.array(counts))
+    x[torch.arange(max_m, device=DEV)[None] >= c[:, None]] = float("nan")      # so may these
     idx = torch.nonzero((torch.arange(max_m, device=DEV)[None] < c[:, None]).view(-1)).view(-1)
     return x, w, b, c, idx, idx // max_m
 
@@ -317,7 +318,7 @@ def run_grouped(counts, K, N, fmt, act, bias=BF, layout="compact", q8=False, pre
     return out, p, os_
 
 
-COUNTS = [[0, 1, 128, 17, 0, 300, 129, 64], [256, 0, 0], [1]]
+COUNTS = [[0, 1, 128, 17, 0, 300, 129, 64], [256, 0, 0], [1], [0, 0]]
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "fp8", "mxfp8", "mxfp4"])
@@ -531,3 +532,66 @@ def test_act_bwd_against_differences(act):
         diff = (vals[0] - vals[1]) / (2 * h) * d.double()
         bound = d.double().abs() * up.double() * (h * h / 2 * 3) + d.double().abs() * (vals[0].abs() + vals[1].abs()) * 2.0 ** -20 / h + 1e-6
         check(dp[:, cols], diff, bound + HALF[BF] * (diff.abs() + bound), (act, part))
+
+
+# --- offsets past 32 bits -----------------------------------------------------------------
+
+def spot_check(x, w, bias, out, pre, act, rows, idx_w=None):
+    """Rows of a large product against 64 bits."""
+    xd = x[rows].double()
+    wd, bd = w.double(), None if bias is None else bias.double()
+    want = xd @ wd.t() + (0 if bd is None else bd)
+    dp = product_bound(xd, wd, bd)
+    check(out[rows], activation(want, act), act_bound(want, dp, act, out.dtype), "out")
+    if pre is not None:
+        check(pre[rows], want, dp + HALF[BF] * (want.abs() + dp), "pre")
+
+
+@pytest.mark.parametrize("T,K,N,act,pre", [(70001, 72, 32768, "gelu", True), (70001, 128, 32768, "swiglu_clamp", True),
+                                           (70001, 32776, 64, "none", False), (70001, 32768, 24, "silu", False),
+                                           (24, 16392, 140000, "relu2", False), (600, 16384, 140032, "none", False)])
+def test_linear_past_32_bits(T, K, N, act, pre):
+    announce("past 32 bits", T, K, N, act)
+    x, w, b = rand(1, T, K), rand(2, N, K, scale=K ** -0.5), rand(3, N)
+    wide = N // 2 if act in GATED else N
+    o = torch.empty(T, wide, dtype=BF, device=DEV)
+    p = torch.empty(T, N, dtype=BF, device=DEV) if pre else None
+    L.moe_linear(x, w, o, bias=b, act=act, pre=p, alpha=ALPHA, limit=LIMIT)
+    rows = torch.tensor(sorted({0, 1, T // 2, T - 2, T - 1} & set(range(T))), device=DEV)
+    spot_check(x, w, b, o, p, act, rows)
+
+
+def test_grouped_and_gradient_past_32_bits():
+    G, K, N = 40, 8192, 8192          # 5.4 GB of weights
+    counts = [0] * 10 + [300] + [0] * 20 + [7] + [0] * 7 + [129]
+    x, w, b, m, idx, e = grouped_inputs(counts, K, N, "bf16", "silu_mul", BF, "compact")
+    out, pre = torch.empty(len(m), N // 2, dtype=BF, device=DEV), torch.empty(len(m), N, dtype=BF, device=DEV)
+    L.grouped_gemm_contig_act(False, x, None, w, None, out, m, bias=b, act="silu_mul", pre=pre)
+    for g in (10, 31, 39):
+        r = idx[e == g]
+        spot_check(x, w[g], b[g], out, pre, "silu_mul", r[:: max(1, len(r) // 5)])
+    xm = torch.zeros(G, 300, K, dtype=BF, device=DEV)
+    om = torch.empty(G, 300, N // 2, dtype=BF, device=DEV)
+    for g in (10, 31, 39):
+        xm[g, :counts[g]] = x[idx[e == g]]
+    L.grouped_gemm_masked_act(False, xm, None, w, None, om, i32_dev(np.array(counts)), 0, bias=b, act="silu_mul")
+    for g in (10, 31, 39):
+        assert torch.equal(om[g, :counts[g]], out[idx[e == g]]), g
+    del x, w, xm, om
+    M, N = 70001, 32768
+    pre, dout = rand(1, M, N), rand(2, M, N // 2)
+    dpre, db = torch.empty_like(pre), torch.empty(N, dtype=F32, device=DEV)
+    L.moe_act_bwd(pre, dout, dpre, "silu_mul", dbias=db)
+    rows = torch.tensor([0, M // 2, M - 1], device=DEV)
+    p, d = pre[rows].double(), dout[rows].double()
+    want, t = exact_bwd(p, d, "silu_mul"), 2.0 ** -20 * bwd_terms(p, d, "silu_mul")
+    check(dpre[rows], want, t + HALF[BF] * (want.abs() + t), "dpre")
+    total = torch.zeros(N, dtype=torch.float64, device=DEV)
+    mag = torch.zeros(N, dtype=torch.float64, device=DEV)
+    for a in range(0, M, 4096):
+        g = exact_bwd(pre[a:a + 4096].double(), dout[a:a + 4096].double(), "silu_mul")
+        total += g.sum(0)
+        mag += g.abs().sum(0) + bwd_terms(pre[a:a + 4096].double(), dout[a:a + 4096].double(), "silu_mul").sum(0) * 2.0 ** -20 * 2.0 ** 24 / M
+    # a sum of M terms in blocks of at most 128 rows and 16 stretches of them: no chain of
+    # additions is longer than 128 + 16 + M / 16 / 16, far below M
+    check(db, total, (M + 4) * 2.0 ** -24 * mag, "dbias")

@@ -209,6 +209,19 @@ def test_backward_of_a_share_and_of_given_ids():
     assert dtw.shape == (200, 4) and torch.equal(c.layer.dgate, before)
 
 
+def test_logits_given_to_a_layer_with_a_router():
+    """The router's gradients stay, dlogits come in rows of E, as without a router."""
+    a, b = Case(train=True, S=0), Case(train=True, S=0, router=False)
+    logits = torch.randn(200, 16, device=DEV)
+    for n in ("w13", "w2"):
+        getattr(b.layer, n).copy_(getattr(a.layer, n))
+    b.layer.set_bias(a.b13, a.b2)
+    assert torch.equal(a.layer(a.x, logits), b.layer(a.x, logits))
+    (dx, dl), (dx2, dl2) = a.layer.backward(a.dout), b.layer.backward(a.dout)
+    assert dl.is_contiguous() and torch.equal(dx, dx2) and torch.equal(dl, dl2)
+    assert (a.layer.dgate == 0).all()
+
+
 def test_training_steps_captured():
     """Forward, backward and AdamW step of the whole layer in a graph, against the same steps run eagerly."""
     def make():

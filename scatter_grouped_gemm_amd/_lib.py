@@ -443,13 +443,15 @@ def _act(act: str) -> int:
 
 def _rows(name: str, dtype, shape, t, dev: int):
     """Data pointer and row stride of a matrix on the current device whose rows are contiguous."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        if t.is_contiguous() or shape[0] <= 1 and (shape[1] <= 1 or t.stride(1) == 1):
+            return t.data_ptr(), shape[1]
+        if shape[1] <= 1 or t.stride(1) == 1:
+            return t.data_ptr(), t.stride(0)
+        raise ValueError(f"{name}: rows must be contiguous")
     if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name}: want {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: is on {t.device}, not on the current device")
-    if shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: rows must be contiguous")
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+    raise ValueError(f"{name}: is on {t.device}, not on the current device")
 
 
 def _bias(bias, shape, dev: int):
@@ -470,33 +472,36 @@ def moe_linear(x, w, out, bias=None, act="none", residual=None, pre=None, alpha=
     code = _act(act)
     T, K = x.shape
     N = w.shape[0]
+    odt = out.dtype
     _need(code < 8 or N % 2 == 0, "moe_linear: a gated activation takes an even number of columns")
-    _need(out.dtype in (_BF16, _F32), "moe_linear: out is bf16 or fp32")
+    _need(odt is _BF16 or odt is _F32, "moe_linear: out is bf16 or fp32")
     dev = _current()
     shape = (T, N // 2 if code >= 8 else N)
     px, ldx = _rows("x", _BF16, (T, K), x, dev)
-    po, ldo = _rows("out", out.dtype, shape, out, dev)
-    pr, ldr = (None, 0) if residual is None else _rows("residual", out.dtype, shape, residual, dev)
+    po, ldo = _rows("out", odt, shape, out, dev)
+    pr, ldr = (None, 0) if residual is None else _rows("residual", odt, shape, residual, dev)
     pb, bdt = _bias(bias, (N,), dev)
     _check("moe_linear", lib().moe_linear(
         px, ldx, _dev("w", _BF16, (N, K), w, dev), pb, bdt, code, alpha, limit, pr, ldr,
-        MOE_DTYPE_FP32 if out.dtype is _F32 else MOE_DTYPE_BF16, po, ldo,
+        MOE_DTYPE_FP32 if odt is _F32 else MOE_DTYPE_BF16, po, ldo,
         None if pre is None else _dev("pre", _BF16, (T, N), pre, dev), T, N, K, _raw_stream(dev)))
 
 
-def _product_operands(name, fp8, A, A_scale, B, B_scale, out, out_scale, rows, K, G, N, K2, cols, per_row, dev):
+def _product_operands(name, fp8, A, A_scale, B, B_scale, out, out_scale, rows, K, G, N, K2, per_row, dev):
     """Pointers of a grouped product's tensors: (A, A_scale, B, B_scale, out dtype, out, out_scale)."""
-    adt = torch.uint8 if fp8 else _BF16
+    if K != K2:
+        raise ValueError(f"{name}: A and B differ in their reduction")
+    if not fp8 and out.dtype is _BF16:
+        return (_dev("A", _BF16, A.shape, A, dev), None, _dev("B", _BF16, B.shape, B, dev), None, MOE_DTYPE_BF16,
+                _dev("out", _BF16, per_row, out, dev), None)
     q8 = out.dtype is torch.uint8
-    _need(K == K2, f"{name}: A and B differ in their reduction")
     _need(q8 or out.dtype is _BF16, f"{name}: out is bf16 or uint8 (e4m3)")
-    u8 = lambda what, t, n: _scale(what, t, n, dev)  # noqa: E731
-    n_scale = rows * (K // 128)
-    w_scale = 0 if not fp8 else G * N * (K // 32) if fp8 in ("mxfp8", "mxfp4") else G * (N // 128) * (K // 128)
-    return (_dev("A", adt, A.shape, A, dev), u8("A_scale", A_scale, n_scale) if fp8 else None,
-            _dev("B", adt, B.shape, B, dev), u8("B_scale", B_scale, w_scale) if fp8 else None,
-            MOE_DTYPE_FP8_E4M3_UE8M0 if q8 else MOE_DTYPE_BF16, _dev("out", out.dtype, per_row + (cols,), out, dev),
-            u8("out_scale", out_scale, rows * (cols // 128)) if q8 else None)
+    adt = torch.uint8 if fp8 else _BF16
+    w_scale = G * N * (K // 32) if fp8 in ("mxfp8", "mxfp4") else G * (N // 128) * (K // 128)
+    return (_dev("A", adt, A.shape, A, dev), _scale("A_scale", A_scale, rows * (K // 128), dev) if fp8 else None,
+            _dev("B", adt, B.shape, B, dev), _scale("B_scale", B_scale, w_scale, dev) if fp8 else None,
+            MOE_DTYPE_FP8_E4M3_UE8M0 if q8 else MOE_DTYPE_BF16, _dev("out", out.dtype, per_row, out, dev),
+            _scale("out_scale", out_scale, rows * (per_row[-1] // 128), dev) if q8 else None)
 
 
 def _scale(name: str, t, n: int, dev: int):
@@ -517,7 +522,7 @@ def grouped_gemm_contig_act(fp8, A, A_scale, B, B_scale, out, m_indices, bias=No
     G, N, K2 = _bk(fp8, B)
     dev = _current()
     ops = _product_operands("grouped_gemm_contig_act", fp8, A, A_scale, B, B_scale, out, out_scale, M, K, G, N, K2,
-                            N // 2 if code >= 8 else N, (M,), dev)
+                            (M, N // 2 if code >= 8 else N), dev)
     pb, bdt = _bias(bias, (G, N), dev)
     _check("grouped_gemm_contig_act", lib().grouped_gemm_contig_act(
         _gemm_dtype(fp8), *ops[:4], pb, bdt, code, alpha, limit, *ops[4:],
@@ -537,7 +542,7 @@ def grouped_gemm_masked_act(fp8, A, A_scale, B, B_scale, out, masked_m, expected
     _need(G == G2, "grouped_gemm_masked_act: A and B differ in their experts")
     dev = _current()
     ops = _product_operands("grouped_gemm_masked_act", fp8, A, A_scale, B, B_scale, out, out_scale, G * max_m, K, G, N,
-                            K2, N // 2 if code >= 8 else N, (G, max_m), dev)
+                            K2, (G, max_m, N // 2 if code >= 8 else N), dev)
     pb, bdt = _bias(bias, (G, N), dev)
     _check("grouped_gemm_masked_act", lib().grouped_gemm_masked_act(
         _gemm_dtype(fp8), *ops[:4], pb, bdt, code, alpha, limit, *ops[4:],

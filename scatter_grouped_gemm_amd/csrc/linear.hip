@@ -1,7 +1,8 @@
 // Products with bias, activation and residual in their epilogue: tiles of BM rows by BN
 // rows of B, four wavefronts of BM/2 by BN/2, for the dense product (moe_linear) and the
 // compact grouped one, where it is too small for linear_wide.hip or has a form that that
-// kernel does not (any N, K a multiple of 8, fp32 output, rows apart).
+// kernel does not (columns or rows that are not whole aligned groups; a residual with
+// a gated activation, a kept product or fp32 output).
 //
 // The sum of an output runs through v_mfma_f32_16x16x32_bf16 over ascending k; a
 // step of 64 takes the 16-byte chunks 0, 2, 4, 6 of a row's 128 bytes in its first

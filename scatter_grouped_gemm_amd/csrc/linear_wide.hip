@@ -33,8 +33,8 @@
 // has no epilogue):
 //   4096 x 4096 x 28672 650 (1480), gated with pre 690; library 624 (1541).  8192 cubed 716
 //   (1534); 666 (1651).  16384 x 1536 x 4096 154 (1340), residual 178; 150 (1377).  8191 x
-//   2048 x 7168 188 (1278), residual 208; 174 (1385).  8000 x 4104 x 8200 469 (1148; K and N
-//   with part steps and columns)
+//   2048 x 7168 188 (1278), residual 208, fp32 out 200; 174 (1385).  8000 x 4104 x 8200 469
+//   (1148; K and N with part steps and columns), fp32 out 535 (128 x 128 tiles 657)
 //   8 experts of 1024 rows, 28672 x 4096 gated with pre 1580 (1220); 128 ragged ones, 4096
 //   x 1536, 131072 rows 1540 (1070)
 // What bounds it: within a tile the card's power (matrix cores busy 80% of the cycles at
@@ -88,10 +88,11 @@ __device__ __forceinline__ u32x4 pack8_add(f32x4 v0, f32x4 v1, u32x4 r) {
 // them, so that leaving out a half would cost more (a branch a phase, 1%) than it gains.
 // TAIL: K is no multiple of 64.  What a row's last step holds behind K is read as 0 by
 // both operands: the lanes that carry it get an offset outside the buffer.
-template <bool GROUPED, bool GATED, bool PRE, bool RES, bool TAIL>
+template <bool GROUPED, bool GATED, bool PRE, bool RES, bool F32, bool TAIL>
 __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  static_assert(!RES || !(GROUPED || GATED || PRE), "no store for gated ones; too many registers with pre");
+  static_assert(!RES || !(GROUPED || GATED || PRE || F32), "no store for gated ones; too many registers with pre or fp32");
+  static_assert(!F32 || !(GROUPED || PRE), "the grouped products have no fp32 output");
   // A half h of stage s, B of stage s.  Arrays of their own: the compiler then knows
   // which loads to LDS a read can depend on.
   __shared__ __attribute__((aligned(1024))) uint8_t p00[16384], p01[16384], p10[16384], p11[16384];
@@ -341,21 +342,26 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
     }
     const int c0 = ct.nt * kCols + wn * (GATED ? 32 : 64);
     const int cols = fresh_copy(a.cols), N = fresh_copy(a.N);
-    const int oline = static_cast<int>(a.ldo) * 2, pline = N * 2;
+    const int oline = static_cast<int>(a.ldo) * (F32 ? 4 : 2), pline = N * 2;
     // of a lane's 16 bytes in a half's 64: a store covers 16 rows.  (Whole lines of eight
     // rows take an exchange between lanes, which costs more than the stores gain: 4096 x
     // 1536, 16384 rows, us 162 and 160, with GELU 202 and 198.)
     const int lc = (g & 1) * 16 + (g >> 1) * 8;
     // columns behind the last one: outside every buffer here (below 2^31 bytes)
     const uint32_t o32[2] = {c0 + lc < cols ? lc * 2u : 0x80000000u, c0 + lc + 32 < cols ? lc * 2u + 64 : 0x80000000u};
+    // fp32: a lane's four columns of a block
+    const auto of = [&](int hq, int j) __attribute__((always_inline)) -> uint32_t {
+      const int c = hq * 32 + j * 16 + g * 4;
+      return c0 + c < cols ? c * 4u : 0x80000000u;
+    };
     // the lines of the quadrants' 64 rows from column col on
-    const auto part = [&](const void* p, int64_t line, int hp, int col) __attribute__((always_inline)) {
+    const auto part = [&](const void* p, int64_t line, int hp, int col, int es = 2) __attribute__((always_inline)) {
       const int r0 = hp * 128 + wm * 64;
       int rows = ct.rows - r0;
       rows = rows < 64 ? rows : 64;
       if (c0 >= cols) rows = 0;
-      return buffer(static_cast<const uint8_t*>(p) + (ct.row + r0) * line + col * 2ll,
-                    rows > 0 ? rows * static_cast<int>(line) - col * 2 : 0);
+      return buffer(static_cast<const uint8_t*>(p) + (ct.row + r0) * line + static_cast<int64_t>(col) * es,
+                    rows > 0 ? rows * static_cast<int>(line) - col * es : 0);
     };
     u32x4 old[2][4][2];
     if constexpr (RES) {  // all in flight together
@@ -383,12 +389,18 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
             __builtin_amdgcn_raw_buffer_store_b128(pack8(acc[hp][1][i][0], acc[hp][1][i][1]), ru, off, 0, 0);
           }
         }
-        const auto rd = part(a.out, oline, hp, c0);
+        const auto rd = part(a.out, oline, hp, c0, F32 ? 4 : 2);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           f32x4 v[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) v[j] = act::gated4(a.act, acc[hp][0][i][j], acc[hp][1][i][j]);
+          if constexpr (F32) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v[j]), rd, (i * 16 + row) * oline + of(0, j), 0, 0);
+            continue;
+          }
           __builtin_amdgcn_raw_buffer_store_b128(pack8(v[0], v[1]), rd, (i * 16 + row) * oline + o32[0], 0, 0);
         }
       } else {
@@ -404,7 +416,18 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
               __builtin_amdgcn_raw_buffer_store_b128(w[h], rd, (i * 16 + row) * pline + o32[h], 0, 0);
           }
         }
-        const auto rd = part(a.out, oline, hp, c0);
+        const auto rd = part(a.out, oline, hp, c0, F32 ? 4 : 2);
+        if constexpr (F32) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              f32x4 v = act::value4(a.act, acc[hp][q >> 1][i][q & 1]);
+              asm volatile("" : "+v"(v));  // one store, not one behind each activation
+              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rd, (i * 16 + row) * oline + of(q >> 1, q & 1), 0, 0);
+            }
+          continue;
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           u32x4 w[2];
@@ -427,7 +450,7 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
   // and the bias too (63 is the counter's limit).  Each wait is for loads whose data is
   // read one phase later: the barrier behind it makes them visible to both groups
   // before the first one reads.
-  constexpr int kStores = (GATED ? 8 : 16) + (PRE ? 16 : 0) + 1;
+  constexpr int kStores = (GATED ? 8 : 16) * (F32 ? 2 : 1) + (PRE ? 16 : 0) + 1;
   constexpr int kW1 = 10 + kStores < 63 ? 10 + kStores : 63, kW2 = 8 + kStores < 63 ? 8 + kStores : 63;
   bool half = false;  // the tile has no rows in its lower half
   // One step from stage S, starting with B's half S.
@@ -508,16 +531,16 @@ __global__ __launch_bounds__(kThreads, 2) void linear_wide_kernel(const LinearAr
 #endif
 }
 
-template <bool GROUPED, bool GATED, bool PRE, bool RES = false>
+template <bool GROUPED, bool GATED, bool PRE, bool RES = false, bool F32 = false>
 int32_t launch(const LinearArgs& a, hipStream_t s) {
   const int grid = linear_cus();  // one workgroup per CU
   if (grid == 0) return MOE_EDEVICE;
   if constexpr (GROUPED)
-    linear_wide_kernel<GROUPED, GATED, PRE, RES, false><<<grid, kThreads, 0, s>>>(a);
+    linear_wide_kernel<GROUPED, GATED, PRE, RES, F32, false><<<grid, kThreads, 0, s>>>(a);
   else if (a.K % kStep == 0)
-    linear_wide_kernel<GROUPED, GATED, PRE, RES, false><<<grid, kThreads, 0, s>>>(a);
+    linear_wide_kernel<GROUPED, GATED, PRE, RES, F32, false><<<grid, kThreads, 0, s>>>(a);
   else
-    linear_wide_kernel<GROUPED, GATED, PRE, RES, true><<<grid, kThreads, 0, s>>>(a);
+    linear_wide_kernel<GROUPED, GATED, PRE, RES, F32, true><<<grid, kThreads, 0, s>>>(a);
   MOE_CHECK_LAUNCH();
   return MOE_OK;
 }
@@ -540,9 +563,10 @@ int linear_cus() {
 
 bool linear_wide_covers(const LinearArgs& a) {
   const int64_t ldb = static_cast<int64_t>(a.K) * 2;
-  return !a.out32 && a.vec8 && !(a.residual && (a.m_indices || a.act.gated || a.pre)) && (!a.m_indices || a.K % kStep == 0) && a.K > kStep &&
+  return (a.out32 ? a.vec && !a.residual && !a.pre && !a.m_indices
+                  : a.vec8 && !(a.residual && (a.m_indices || a.act.gated || a.pre))) && (!a.m_indices || a.K % kStep == 0) && a.K > kStep &&
          // 32-bit offsets: 256 rows of A, out and pre, of B 256 rows or (gated) half of all
-         a.lda <= (1 << 22) && a.ldo <= (1 << 21) && a.ldr <= (1 << 21) && a.N <= (1 << 21) &&
+         a.lda <= (1 << 22) && a.ldo <= (1 << (a.out32 ? 20 : 21)) && a.ldr <= (1 << 21) && a.N <= (1 << 21) &&
          (a.act.gated ? (static_cast<int64_t>(a.cols) + 256) * ldb < (1ll << 32) : a.K <= (1 << 21)) &&
          // run table and tile positions
          (a.m_indices ? (a.M + 127) / 128 <= runs::kMaxBlocks && a.G <= 1024 : true) &&
@@ -554,6 +578,8 @@ int32_t launch_linear_wide(const LinearArgs& a, hipStream_t s) {
     if (a.act.gated) return a.pre ? launch<true, true, true>(a, s) : launch<true, true, false>(a, s);
     return a.pre ? launch<true, false, true>(a, s) : launch<true, false, false>(a, s);
   }
+  if (a.out32)
+    return a.act.gated ? launch<false, true, false, false, true>(a, s) : launch<false, false, false, false, true>(a, s);
   if (a.act.gated) return a.pre ? launch<false, true, true>(a, s) : launch<false, true, false>(a, s);
   if (a.residual) return launch<false, false, false, true>(a, s);
   return a.pre ? launch<false, false, true>(a, s) : launch<false, false, false>(a, s);

@@ -62,7 +62,7 @@ def _no_spills(found, text, n):
 
 
 def test_no_register_is_spilled(wide, thin, tile):
-    _no_spills(*wide, 14)    # (grouped, gated, pre, residual, tail)
+    _no_spills(*wide, 18)    # (grouped, gated, pre, residual, fp32, tail)
     _no_spills(*thin, 12)    # (loads of A, blocks of 16 rows of B, gated)
     _no_spills(*tile, 8)     # (BM, BN, stages, gated)
 
@@ -91,9 +91,9 @@ def test_loads_of_a_wide_step_are_where_its_waits_count_them(wide):
 
 def test_stores_of_a_wide_epilogue(wide):
     for key, lines in wide[0].items():
-        grouped, gated, pre, res, tail = key
+        grouped, gated, pre, res, f32, tail = key
         n = sum(line.startswith("buffer_store_dwordx4") for line in lines)
-        assert n == (8 if gated else 16) + (16 if pre else 0), (key, n)
+        assert n == (8 if gated else 16) * (2 if f32 else 1) + (16 if pre else 0), (key, n)
         others = [line for line in lines if re.match(r"(global|flat)_store|buffer_store(?!_dwordx4)|global_atomic", line)]
         assert not others, (key, others[:3])
         bias = sum(_to_lds(line, "dword") for line in lines)

@@ -85,6 +85,24 @@ def test_linear_large_and_odd(T, K, N, act, residual, pre, pad):
     run_linear(T, K, N, act, BF, residual, BF, pre, pad, seed=T)
 
 
+@pytest.mark.parametrize("T,K,N,act,pad", [(4100, 256, 4100, "none", 0), (3000, 200, 6152, "gelu", 12), (2600, 328, 8216, "silu_mul", 4),
+                                           (2500, 448, 10248, "swiglu_clamp", 0)])
+def test_linear_large_fp32(T, K, N, act, pad):
+    """fp32 out of the large tiles, columns and rows of groups of four."""
+    announce("large fp32", T, K, N, act, pad)
+    x, w, b, _, o, _ = linear_case(T, K, N, act, F32, False, F32, False, 0)
+    wide = N // 2 if act in GATED else N
+    o = torch.full((T + 1, wide + pad), GUARD, device=DEV)
+    L.moe_linear(x, w, o[:T, :wide], bias=b, act=act, alpha=ALPHA, limit=LIMIT)
+    want = x.double() @ w.double().t() + b.double()
+    dp = product_bound(x.double(), w.double(), b.double())
+    check(o[:T, :wide], activation(want, act), act_bound(want, dp, act, F32), "out")
+    assert (o[T:] == GUARD).all() and (o[:, wide:] == GUARD).all()
+    small = torch.empty(40, wide, device=DEV)
+    L.moe_linear(x[:40], w, small, bias=b, act=act, alpha=ALPHA, limit=LIMIT)
+    assert torch.equal(small, o[:40, :wide])
+
+
 @pytest.mark.parametrize("K,N", [(1000, 4360), (456, 5000)])
 def test_linear_odd_rows_do_not_depend_on_each_other(K, N):
     w, x = rand(1, N, K, scale=K ** -0.5), rand(3, 4000, K)

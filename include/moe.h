@@ -542,7 +542,8 @@ size_t moe_act_bwd_ws_bytes(int64_t M, int32_t N, int32_t G);
  *                NULL: the bias gradient alone
  *   dout         dout_dtype MOE_DTYPE_BF16 or MOE_DTYPE_FP32 (as the output was): [M][N],
  *                [M][N/2] with a gated activation
- *   expert_start_loc, num_valid   device int32 [G], needed with m_indices and dbias
+ *   expert_start_loc, num_valid   device int32 [G] as moe_scatter_compact writes them,
+ *                needed with m_indices and dbias
  *   dbias        dbias_dtype MOE_DTYPE_BF16 or MOE_DTYPE_FP32 [G][N], or NULL.  An
  *                expert without rows gets 0 (or keeps what it holds)
  *   ws, ws_bytes scratch for dbias, at least moe_act_bwd_ws_bytes(M, N, G); calls that

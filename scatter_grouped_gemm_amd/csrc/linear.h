@@ -43,7 +43,6 @@ void linear_alignment(LinearArgs& a);
 namespace {
 
 typedef __attribute__((ext_vector_type(2))) uint32_t lin_u32x2;
-typedef __attribute__((ext_vector_type(4))) uint32_t lin_u32x4;
 typedef __attribute__((ext_vector_type(4))) float lin_f4;
 
 __device__ __forceinline__ lin_f4 unpack_bf16x4(lin_u32x2 b) {

@@ -534,6 +534,7 @@ size_t moe_act_bwd_ws_bytes(int64_t M, int32_t N, int32_t G);
  *                 rounded once to its type
  * At a gate or up part that equals its limit the cut passes the gradient on, past
  * it the part's gradient is 0.
+ * act' of a NaN is one; at the infinities it is its limit (0 and, but for RELU2, 1).
  *   Rows: m_indices (compact), masked_m with max_m (masked; M = G*max_m) or, both
  *   NULL, every row (then G = 1).  Other rows of dpre are left as they were and are
  *   part of no sum.

@@ -35,8 +35,12 @@ namespace act {
 
 typedef __attribute__((ext_vector_type(4))) float f4;
 
-// Far out sigma is 0 or 1 whatever x; cut there, x^3 stays finite and 0 times it 0.
-__device__ __forceinline__ float bounded(float x) { return fminf(fmaxf(x, -1e12f), 1e12f); }
+// Far out sigma is 0 or 1 whatever x; cut there, x^3 stays finite and 0 times it 0.  By
+// the minimum and maximum that keep a NaN (one instruction each, as fminf and fmaxf are,
+// which drop it): the derivative is made of nothing but the value cut here.
+__device__ __forceinline__ float bounded(float x) {
+  return __builtin_elementwise_minimum(__builtin_elementwise_maximum(x, -1e12f), 1e12f);
+}
 
 __device__ __forceinline__ float sigmoid(const ActArgs& a, float x) {
   const float xb = bounded(x);

@@ -298,6 +298,9 @@ class MoELayer:
         if (self.expert_bias and self.b13 is None) or (self.S and self.shared_w13 is None):
             self._check_extras()
         own_logits = topk_ids is None and logits is None
+        keep_x = self.train and (bool(self.S) or own_logits)
+        if keep_x and x.untyped_storage().data_ptr() == self.out.untyped_storage().data_ptr():
+            raise ValueError("x is the layer's own output buffer: backward needs it as it was, give a copy")
         if own_logits:
             with self._mark("router"):
                 logits = self.router_logits(x)
@@ -369,16 +372,17 @@ class MoELayer:
                     L.grouped_gemm_masked(wdt, act3, self.act_scale, self.w2, self.w2_scale,
                                           self.y.view(El, mm, self.H), self.masked_m, self.expected_m)
         out = self.out[:T]
-        with self._mark("combine"):
-            L.moe_combine(self.y, s2d, tw, out)
-        if self.S:
+        if self.S:               # before the combine: x may be what the last forward returned
             with self._mark("shared_w13"):
                 L.moe_linear(x, self.shared_w13, self.shared_act[:T], act=self.activation,
                              pre=self.shared_pre[:T] if self.train else None, **self.act_args)
+        with self._mark("combine"):
+            L.moe_combine(self.y, s2d, tw, out)
+        if self.S:
             with self._mark("shared_w2"):
                 L.moe_linear(self.shared_act[:T], self.shared_w2, out, residual=out)
         if self.train:
-            self._saved = (T, ids, tw, topk_ids is None, own_logits, x if self.S or own_logits else None)
+            self._saved = (T, ids, tw, topk_ids is None, own_logits, x if keep_x else None)
         return out
 
     __call__ = forward

@@ -125,6 +125,7 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(const ActBwdArgs a) {
   const int tid = threadIdx.x;
   const int sub = tid / a.lanes, col = tid % a.lanes, rows_at_once = 256 / a.lanes;
   const int64_t block = blockIdx.x;
+  const int chunk = blockIdx.z * gridDim.y + blockIdx.y;  // of the columns; of the last ones some may be behind them
   int64_t row0, end;
   if constexpr (WHOLE) {
     rows_of(a, static_cast<int>(block), row0, end);
@@ -145,7 +146,7 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(const ActBwdArgs a) {
     }
     if (row0 >= end) return;
   }
-  const int c = (blockIdx.y * a.lanes + col) * 8;
+  const int c = (chunk * a.lanes + col) * 8;
   float sg[8] = {}, su[8] = {};
   if (c < a.cols)
     for (int64_t r = row0 + sub; r < end; r += rows_at_once) one_row<GATED>(a, r, c, sg, su);
@@ -161,7 +162,7 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(const ActBwdArgs a) {
   const int n = a.lanes * 8;  // columns of this workgroup
   for (int i = tid; i < n * H; i += 256) {
     const int h = i / n, x = i - h * n, q = x >> 3, e = x & 7;
-    const int at = blockIdx.y * n + x;
+    const int at = chunk * n + x;
     if (at >= a.cols) continue;
     float t = 0.0f;
     for (int k = 0; k < rows_at_once; ++k) t += sums[(h * 8 + e) * 256 + k * a.lanes + q];
@@ -213,8 +214,12 @@ int block_rows(int64_t M, int64_t chunks) {
 // second launch for the sums 14).
 bool few_rows(int64_t M, int G) { return M <= 128ll * G && M <= 1024; }
 
+// rows: workgroups in the first dimension.  The chunks of a row's columns are more than the
+// second one holds (65535) from 8 M columns on.
 template <bool WHOLE>
-void launch(const ActBwdArgs& a, dim3 grid, hipStream_t s) {
+void launch(const ActBwdArgs& a, int64_t rows, hipStream_t s) {
+  const int chunks = (a.cols / 8 + a.lanes - 1) / a.lanes, y = chunks < 65535 ? chunks : 65535;
+  const dim3 grid(static_cast<unsigned>(rows), static_cast<unsigned>(y), static_cast<unsigned>((chunks + y - 1) / y));
   if (a.act.gated) act_bwd_kernel<true, WHOLE><<<grid, 256, 0, s>>>(a);
   else act_bwd_kernel<false, WHOLE><<<grid, 256, 0, s>>>(a);
 }
@@ -273,7 +278,7 @@ extern "C" int32_t moe_act_bwd(const void* pre, int32_t dout_dtype, const void* 
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (dbias && few_rows(M, G)) {
     a.lanes = 16;
-    launch<true>(a, dim3(static_cast<unsigned>(G), static_cast<unsigned>((groups + 15) / 16)), s);
+    launch<true>(a, G, s);
     MOE_CHECK_LAUNCH();
     return MOE_OK;
   }
@@ -282,9 +287,8 @@ extern "C" int32_t moe_act_bwd(const void* pre, int32_t dout_dtype, const void* 
   a.nb = masked_m ? (max_m + a.R - 1) / a.R : 0;
   if (M > 0) {
     const int64_t blocks = masked_m ? M / max_m * a.nb : (M + a.R - 1) / a.R;
-    const int64_t cy = (groups + a.lanes - 1) / a.lanes;
-    if (blocks >= (1 << 24) || cy > 65535) return MOE_EUNSUPPORTED;  // a launch's threads and grid
-    launch<false>(a, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(cy)), s);
+    if (blocks >= (1 << 24)) return MOE_EUNSUPPORTED;  // threads of a launch
+    launch<false>(a, blocks, s);
     MOE_CHECK_LAUNCH();
   }
   if (dbias) {

@@ -424,7 +424,8 @@ int32_t moe_combine(const void* Y, int64_t num_rows, const int32_t* src2dst,
  *                MOE_DTYPE_FP32), or NULL
  *   act, alpha, limit   see MOE_ACT_*; the output has N columns, N/2 with a gated one
  *   residual     device, of out's type, row m at residual + m*ld_residual, or NULL.
- *                May be out itself with ld_out, not otherwise overlap it
+ *                May be out itself with ld_out, not otherwise overlap it, and holds no
+ *                element of pre
  *   out          device, out_dtype MOE_DTYPE_BF16 or MOE_DTYPE_FP32, row m at
  *                out + m*ld_out
  *   pre          device bf16 [M][N], out: p for moe_act_bwd, or NULL

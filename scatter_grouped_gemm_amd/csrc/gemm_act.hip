@@ -29,7 +29,7 @@ int32_t act_args(int32_t dtype, const void* A, const uint8_t* A_scale, const voi
   const int32_t st = validate_gemm(dtype, A, A_scale, B, B_scale, out, N, K, G);
   if (st != MOE_OK) return st;
   if (M == 0) return MOE_OK;
-  if (out == A || out == B || (pre && (pre == A || pre == B || pre == out))) return MOE_EINVAL;
+  if (out == A || out == B || out == bias || (pre && (pre == A || pre == B || pre == out || pre == bias))) return MOE_EINVAL;
   if (!rowinfo || (out_dtype == MOE_DTYPE_FP8_E4M3_UE8M0 && !out_scale)) return MOE_EINVAL;
   if (!aligned16(A) || !aligned16(B) || !aligned16(bias) || !aligned16(out) || !aligned16(pre)) return MOE_EUNSUPPORTED;
   a.A = static_cast<const uint8_t*>(A);

@@ -282,7 +282,8 @@ extern "C" int32_t moe_linear(const void* A, int64_t lda, const void* B, const v
   if (M >= (1ll << 31) || (M + 127) / 128 * ((static_cast<int64_t>(N) + 127) / 128) >= (1 << 24)) return MOE_EUNSUPPORTED;
   if (M == 0) return MOE_OK;
   if (!A || !B || !out) return MOE_EINVAL;
-  if (out == A || out == B || pre == A || pre == B || pre == out) return MOE_EINVAL;
+  if (out == A || out == B || out == bias || (pre && (pre == A || pre == B || pre == out || pre == bias || pre == residual)))
+    return MOE_EINVAL;
   if (residual == out && ld_residual != ld_out && M > 1) return MOE_EINVAL;
   if (!aligned(A, 16) || !aligned(B, 16)) return MOE_EUNSUPPORTED;
   a.out32 = out_dtype == MOE_DTYPE_FP32;

@@ -541,7 +541,8 @@ size_t moe_act_bwd_ws_bytes(int64_t M, int32_t N, int32_t G);
  *   part of no sum.
  *   pre, dpre    bf16 [M][N]; dpre may be pre, and may be a bf16 dout where the
  *                activation is not gated.  With MOE_ACT_NONE pre is not read, and dpre may be
- *                NULL: the bias gradient alone
+ *                NULL: the bias gradient alone.  dpre and dbias share memory with
+ *                nothing else
  *   dout         dout_dtype MOE_DTYPE_BF16 or MOE_DTYPE_FP32 (as the output was): [M][N],
  *                [M][N/2] with a gated activation
  *   expert_start_loc, num_valid   device int32 [G] as moe_scatter_compact writes them,

@@ -258,6 +258,8 @@ extern "C" int32_t moe_act_bwd(const void* pre, int32_t dout_dtype, const void* 
   if (dbias && !ws && moe_act_bwd_ws_bytes(M, N, G) > 0) return MOE_EINVAL;
   if (!aligned16(pre) || !aligned16(dout) || !aligned16(dpre) || !aligned16(dbias) || !aligned16(ws)) return MOE_EUNSUPPORTED;
   if (M == 0 && (!dbias || accumulate)) return MOE_OK;
+  if (M > 0 && dpre == dout && (a.act.gated || dout_dtype == MOE_DTYPE_FP32)) return MOE_EINVAL;  // other places for the same element
+  if (M > 0 && dbias && (dbias == dpre || dbias == dout || (a.act.kind != kActNone && dbias == pre))) return MOE_EINVAL;
   a.pre = a.act.kind == kActNone ? nullptr : static_cast<const uint16_t*>(pre);
   a.dout = dout;
   a.dout32 = dout_dtype == MOE_DTYPE_FP32;

@@ -3,7 +3,7 @@ GPU: every call here fails validation, so nothing is launched)."""
 import pytest
 
 from scatter_grouped_gemm_amd import _lib as L
-from test_epilogue_host import P, contig, linear, masked
+from test_epilogue_host import P, bwd, contig, linear, masked
 
 
 @pytest.mark.parametrize("kw", [
@@ -18,3 +18,11 @@ def test_linear_refuses_outputs_that_are_inputs(kw):
 @pytest.mark.parametrize("kw", [dict(bias=3 * P), dict(pre=5 * P, bias=5 * P)])
 def test_grouped_refuses_outputs_that_are_inputs(call, kw):
     assert call(**kw) == L.MOE_EINVAL
+
+
+@pytest.mark.parametrize("kw", [
+    dict(act=9, dpre=2 * P), dict(act=1, odt=16, dpre=2 * P),      # dpre in dout's place, where an element has another one
+    dict(act=1, db=P, dpre=3 * P), dict(act=1, db=2 * P, dpre=3 * P), dict(act=1, db=3 * P, dpre=3 * P),
+])
+def test_act_bwd_refuses_outputs_that_are_inputs(kw):
+    assert bwd(pre=P, dout=2 * P, **kw) == L.MOE_EINVAL

@@ -29,8 +29,8 @@ Beside the experts: ``router=True`` gives the layer the router's own product
 added to the routed experts' output (its second product takes that as its
 residual); ``expert_bias`` and ``activation`` other experts than plain
 SiLU-and-mul ones (grouped_gemm_*_act).  Router and shared expert are BF16 in
-every layer.  Where the experts are shared out over several layers, one of them has
-the shared expert, since their outputs are added up.
+every layer.  Where the experts are shared out over several layers, all of them have
+the same router, and one the shared expert, since their outputs are added up.
 """
 from __future__ import annotations
 
@@ -428,11 +428,12 @@ class MoELayer:
         buffers (dlogits of the layer's own router a slice of wider rows).  Where forward
         was given logits or ids, the router's gradients are left as they are.
 
-        With a share of the experts, dx and dlogits are that share's part: both
-        add up over the shares.  What forward kept is used up: one backward for
-        each forward that came to its end, and ids and weights given to forward (with
-        a router or a shared expert x too) must still be as they were.  With a share of
-        the experts the shared expert and the router's bias belong to one share alone."""
+        With a share of the experts, dx, dlogits and the router's gradients are that share's
+        part: they add up over the shares.  Every share holds the same router, bias included
+        (it takes part in the choice of the experts); the shared expert is given to one of
+        them alone.  What forward kept is used up: one backward for each forward that came to
+        its end, and ids and weights given to forward (with a router or a shared expert x too)
+        must still be as they were."""
         if not self.train:
             raise ValueError("the layer was made without train=True")
         if self._saved is None:

@@ -43,3 +43,39 @@ def test_training_on_its_own_output_without_extras():
     c.layer(c.x, logits)
     assert torch.equal(c.layer(c.layer.out, logits), want)
     assert torch.equal(c.layer.backward(c.dout)[0], dx)
+
+
+def test_shares_add_up_to_the_whole():
+    """Two layers with a part of the experts each and the same router, one of them with the
+    shared expert: outputs, dx, dlogits and the router's gradients are parts of the whole's."""
+    whole = Case(train=True, grad_dtype=F32)
+    shares = []
+    for start, El, S in ((0, 5, 256), (5, 11, 0)):
+        c = Case(train=True, grad_dtype=F32, El=El, start=start, S=S)
+        c.layer.set_weights(whole.w13[start:start + El], whole.w2[start:start + El])
+        c.layer.set_bias(whole.b13[start:start + El], whole.b2[start:start + El])
+        c.layer.set_router(whole.gate, whole.gate_bias)
+        if S:
+            c.layer.set_shared(whole.s13, whole.s2)
+        shares.append(c)
+    got = []
+    for c in shares:
+        out = c.layer(whole.x)
+        dx, dlogits = c.layer.backward(whole.dout)
+        got.append(dict(out=out, dx=dx, dlogits=dlogits, dgate=c.layer.dgate[:16], dgate_bias=c.layer.dgate_bias[:16]))
+    ids = shares[0].layer.topk_ids
+    assert torch.equal(ids, shares[1].layer.topk_ids)
+    p = whole.leaves()
+    out = whole.exact(p, ids)
+    out.backward(whole.dout.double())
+    want = dict(out=out.detach(), dx=p["x"].grad, dgate=p["gate"].grad, dgate_bias=p["gate_bias"].grad)
+    # dlogits: those of the same weights in one layer
+    whole.layer(whole.x)
+    want["dlogits"] = whole.layer.backward(whole.dout)[1].double()
+    for n, w in want.items():
+        a, b = (g[n].double() for g in got)
+        # the whole's bounds (4 roundings forward, 5 on dx's way, the router's differences), each
+        # relative to the part that was rounded; two layers' dlogits are compared with each other
+        tol = {"out": 4 * 2 ** -9, "dx": 0.012}.get(n, 0.04) * (2 if n == "dlogits" else 1)
+        assert (a + b - w).norm() <= tol * (a.norm() + b.norm()), n
+        assert a.norm() > 0.1 * w.norm() and b.norm() > 0.1 * w.norm(), n

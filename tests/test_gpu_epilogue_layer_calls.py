@@ -3,9 +3,9 @@ around it: on its own output, in shares, with batches of other sizes."""
 import pytest
 import torch
 
-from scatter_grouped_gemm_amd import MoELayer
+from epilogue_util import activation
 from gpu_util import DEV, announce
-from test_gpu_epilogue_layer import Case
+from test_gpu_epilogue_layer import Case, check_grads, off
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -79,3 +79,64 @@ def test_shares_add_up_to_the_whole():
         tol = {"out": 4 * 2 ** -9, "dx": 0.012}.get(n, 0.04) * (2 if n == "dlogits" else 1)
         assert (a + b - w).norm() <= tol * (a.norm() + b.norm()), n
         assert a.norm() > 0.1 * w.norm() and b.norm() > 0.1 * w.norm(), n
+
+
+def left(c, back):
+    """Copies of what a step returned and left in the layer."""
+    return [t.clone() for t in (c.layer.out[:len(back[0])], *back, *c.layer.gradients())]
+
+
+@pytest.mark.parametrize("own", ["router", "logits", "ids"])
+@pytest.mark.parametrize("T", [77, 33, 129])
+def test_a_batch_after_a_longer_one(own, T):
+    """Nothing of a longer batch before, or of what the buffers held, is in a shorter one's
+    output and gradients."""
+    announce("shorter batch", own, T)
+    c, fresh = Case(train=True), Case(train=True)
+    for n in ("x_buf", "gateup", "act", "y", "out", "logits", "shared_act", "shared_pre", "shared_dact", "dy", "dx", "dx_parts",
+              "dlogits", "dlogits16", "dtopk_weights", "src2dst"):
+        getattr(fresh.layer, n).view(torch.uint8).fill_(0xFF)
+    c.layer(c.x)
+    c.layer.backward(c.dout)
+    found = []
+    for case in (c, fresh):
+        case.x, case.dout = case.x[:T].contiguous(), case.dout[:T].contiguous()
+        logits = (case.x.double() @ case.gate.double().t() + case.gate_bias.double()).float()
+        if own == "ids":
+            weights, ids = torch.topk(torch.softmax(logits, 1), case.k)
+            ids, weights = ids.int(), (weights / weights.sum(1, keepdim=True)).contiguous()
+            case.layer.topk_ids[:T] = ids
+            case.layer(case.x, topk_ids=ids, topk_weights=weights)
+        else:
+            case.layer(case.x, *(() if own == "router" else (logits,)))
+        if own != "router":                         # what a backward of given logits leaves alone
+            case.layer.allocate_grads()
+        found.append(left(case, case.layer.backward(case.dout)))
+    assert all(torch.equal(a, b) for a, b in zip(*found))
+    p = c.leaves()
+    out = c.exact(p, c.layer.topk_ids[:T])
+    out.backward(c.dout.double())
+    assert off(c.layer.out[:T], out.detach()) < 4 * 2 ** -9
+    if own == "router":
+        check_grads(c, c.layer.dx[:T], p)
+    else:                                           # the router's part of dx is not in it
+        q = {n: t for n, t in c.leaves().items() if not n.startswith("gate")}
+        check_grads(c, c.layer.dx[:T], experts_alone(c, q))
+        assert (c.layer.dgate == 0).all() and (c.layer.dgate_bias == 0).all()
+
+
+def experts_alone(c, q):
+    """c's leaves without the router's, with the gradients of a routing that does not depend on x."""
+    fixed = Case.leaves(c)
+    ids = c.layer.topk_ids[:len(c.x)]
+    full = dict(q, gate=fixed["gate"].detach(), gate_bias=fixed["gate_bias"].detach())
+    frozen = q["x"].detach() @ full["gate"].t() + full["gate_bias"]
+    top = torch.softmax(torch.gather(frozen, 1, ids.long()), 1)
+    out = torch.zeros_like(q["x"])
+    for e in range(c.E):
+        t, j = torch.nonzero(ids == e, as_tuple=True)
+        pre = q["x"][t] @ q["w13"][e].t() + q["b13"][e]
+        out = out.index_add(0, t, top[t, j][:, None] * (activation(pre, c.act) @ q["w2"][e].t() + q["b2"][e]))
+    out = out + activation(q["x"] @ q["s13"].t(), c.act) @ q["s2"].t()
+    out.backward(c.dout.double())
+    return q

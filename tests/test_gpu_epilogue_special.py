@@ -98,3 +98,20 @@ def test_not_finite_products_kept(act, counts, layout):
         s = want.sum(0)
         bound = t.sum(0) + (counts[g] + 4) * 2.0 ** -24 * (want.abs() + t).sum(0)
         same(dbias[g], s, bound + HALF[F32] * (s.abs() + bound), ("dbias", g))
+
+
+@pytest.mark.parametrize("T", [1, 33])
+def test_the_tail_of_gelu(T):
+    """x Phi(x) of negative x keeps a relative error of 4e-7 (Phi(-t) exp(t^2/2) as a polynomial,
+    in fp32), t^2 / 2 times 2.75 places of 2^-24 (two products and a constant rounded in the
+    exponential's argument), two of 2^-23 (exponential, reciprocal) and two of 2^-24 (the last
+    products).  An identity weight passes x through."""
+    x = torch.cat([torch.arange(-12.75, -1, 1 / 16), torch.arange(-1, 0, 1 / 128)]).to(BF)
+    n = len(x) // 8 * 8
+    x = x[:n].to(DEV)
+    o = torch.empty(T, n, dtype=F32, device=DEV)
+    L.moe_linear(x[None].expand(T, n).contiguous(), torch.eye(n, dtype=BF, device=DEV), o, act="gelu")
+    t = -x.double()
+    want = -t * 0.5 * torch.special.erfc(t / math.sqrt(2))
+    bound = 4e-7 + 1.375 * t * t * 2.0 ** -24 + 2 * 2.0 ** -23 + 2 * 2.0 ** -24
+    assert ((o.double() / want - 1).abs() <= bound).all(), float(((o.double() / want - 1).abs() / bound).max())

@@ -101,3 +101,46 @@ def test_bias_gradients_of_many_columns(layout, counts, N, act, db, acc):
             total = total + old[g]
             bound = bound + 2.0 ** -24 * (total.abs() + bound)
         check(dbias[g], total, bound + HALF[db] * (total.abs() + bound), ("dbias", g))
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "mxfp8", "mxfp4"])
+@pytest.mark.parametrize("layout", ["compact", "masked"])
+@pytest.mark.parametrize("act,q8", [("none", False), ("swiglu_clamp", False), ("silu_mul", True)])
+def test_quantised_rows_without_an_assignment_hold_anything(fmt, layout, act, q8):
+    """NaN codes and NaN scales in rows that hold no assignment: the others' outputs keep their bits."""
+    announce("padding", fmt, layout, act, q8)
+    counts, K, N = [0, 1, 128, 17, 200], 384, 512
+    G, wide, max_m = len(counts), N // 2 if act in GATED else N, 205
+    if layout == "compact":
+        m = compact_layout(counts)
+        rows, valid = len(m), torch.from_numpy(m).to(DEV) >= 0
+    else:
+        rows = G * max_m
+        valid = (torch.arange(max_m, device=DEV)[None] < i32_dev(np.array(counts))[:, None]).view(-1)
+    x, w, b = rand(1, rows, K), rand(2, G, N, K, scale=1.5 * K ** -0.5), rand(3, G, N)
+    q, s = torch.empty(rows, K, dtype=torch.uint8, device=DEV), torch.empty(K // 128, rows, dtype=torch.uint8, device=DEV)
+    L.moe_quant_fp8_ue8m0(x, q, s)
+    if fmt == "fp8":
+        wq, ws = torch.empty(w.shape, dtype=torch.uint8, device=DEV), torch.empty(G, N // 128, K // 128, dtype=torch.uint8, device=DEV)
+        L.moe_quant_weight_fp8_ue8m0(w, wq, ws)
+    else:
+        wq = torch.empty(G, N, K // (2 if fmt == "mxfp4" else 1), dtype=torch.uint8, device=DEV)
+        ws = torch.empty(G, N // 64, K // 128, 256, dtype=torch.uint8, device=DEV)
+        L.moe_quant_weight_mx(w, "e2m1" if fmt == "mxfp4" else "e4m3", wq, ws)
+    found = []
+    for spoilt in (False, True):
+        if spoilt:
+            q[~valid], s[:, ~valid] = 0x7F, 0xFF
+        out = torch.full((rows, wide), 0x5A, dtype=torch.uint8, device=DEV) if q8 else torch.full((rows, wide), GUARD, dtype=BF, device=DEV)
+        os_ = torch.full((wide // 128 * rows,), 0x5A, dtype=torch.uint8, device=DEV) if q8 else None
+        kw = dict(bias=b, act=act, out_scale=os_, alpha=ALPHA, limit=LIMIT)
+        if layout == "compact":
+            L.grouped_gemm_contig_act(fmt if fmt != "fp8" else True, q, s, wq, ws, out, i32_dev(m), **kw)
+        else:
+            L.grouped_gemm_masked_act(fmt if fmt != "fp8" else True, q.view(G, max_m, K), s.view(K // 128, G, max_m).transpose(0, 1).contiguous(),
+                                      wq, ws, out.view(G, max_m, wide), i32_dev(np.array(counts)), 0, **kw)
+        torch.cuda.synchronize()
+        assert (out[~valid] == (0x5A if q8 else GUARD)).all()
+        found.append((out, os_))
+    assert torch.equal(found[0][0], found[1][0]) and (not q8 or torch.equal(found[0][1], found[1][1]))
+    assert q8 or not torch.isnan(found[0][0].float()).any()

@@ -408,9 +408,10 @@ int32_t moe_combine(const void* Y, int64_t num_rows, const int32_t* src2dst,
                     void* stream);
 
 /* ---------------------------------------------------------------------------
- * Products with an epilogue.  The product is summed in fp32 over ascending k, and
- * bias, activation and residual follow in fp32 before the one rounding to the
- * output's type.  A row's result depends on its own row and its weights alone: it
+ * Products with an epilogue.  The product is summed in fp32 over ascending k (with
+ * quantised weights the products of 128 of k by the matrix core, to about 2^-15 of the
+ * largest, and these sums in fp32), and bias, activation and residual follow in fp32
+ * before the one rounding to the output's type.  A row's result depends on its own row and its weights alone: it
  * is the same for any number of rows, and in both layouts.
  * ------------------------------------------------------------------------- */
 

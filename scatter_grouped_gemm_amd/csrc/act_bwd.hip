@@ -210,8 +210,8 @@ int block_rows(int64_t M, int64_t chunks) {
 }
 
 // Few rows an expert: one launch, in which each workgroup takes all rows of an expert by
-// 128 columns, 16 rows at a time.  us (N 1024, gated): 8 experts of 8 rows 11 (with a
-// second launch for the sums 14).
+// 128 columns, 16 rows at a time.  us (N 1024, gated): 8 experts of 8 rows 9.5 (with a
+// second launch for the sums 13.9).
 bool few_rows(int64_t M, int G) { return M <= 128ll * G && M <= 1024; }
 
 // rows: workgroups in the first dimension.  The chunks of a row's columns are more than the

@@ -235,7 +235,8 @@ void linear_alignment(LinearArgs& a) {
            (!a.residual || (a.ldr % 8 == 0 && aligned(a.residual, 16))) && (!a.pre || aligned(a.pre, 16));
 }
 
-// Which kernel takes a call, by the tiles that each would have; the bits are the same.
+// Which kernel takes a call, by the tiles that each would have (in the compact layout by
+// the buffers' height: the rows in them are on the device); the bits are the same.
 // us, one matrix, K 4096 (7168 where marked):
 //   up to 32 rows, the thin kernel: 1 row, N 4096* 12 (64 x 64 tiles 32), N 16384* 35 (40);
 //     with wider N the 64 x 64 tiles' reads are as good, and they read A less often (32

@@ -248,11 +248,10 @@ extern "C" int32_t moe_act_bwd(const void* pre, int32_t dout_dtype, const void* 
   if (dout_dtype != MOE_DTYPE_BF16 && dout_dtype != MOE_DTYPE_FP32) return MOE_EUNSUPPORTED;
   if (masked_m && m_indices) return MOE_EINVAL;
   if (masked_m && (max_m <= 0 || M % max_m != 0 || (dbias && M / max_m != G))) return MOE_EINVAL;
-  if (!masked_m && !m_indices && G != 1) return MOE_EINVAL;
+  if (M > 0 && !masked_m && !m_indices && G != 1) return MOE_EINVAL;  // tensors without elements have no address
   if (dbias && dbias_dtype != MOE_DTYPE_BF16 && dbias_dtype != MOE_DTYPE_FP32) return MOE_EUNSUPPORTED;
   if (dbias && m_indices && (!expert_start_loc || !num_valid)) return MOE_EINVAL;
-  if (a.act.kind != kActNone && !dpre) return MOE_EINVAL;
-  if (!dpre && !dbias) return MOE_EINVAL;
+  if (M > 0 && !dpre && (a.act.kind != kActNone || !dbias)) return MOE_EINVAL;
   if (M > 0 && (!dout || (a.act.kind != kActNone && !pre))) return MOE_EINVAL;
   if (dbias && ws_bytes < moe_act_bwd_ws_bytes(M, N, G)) return MOE_ECAPACITY;
   if (dbias && !ws && moe_act_bwd_ws_bytes(M, N, G) > 0) return MOE_EINVAL;

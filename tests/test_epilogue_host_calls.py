@@ -26,3 +26,11 @@ def test_grouped_refuses_outputs_that_are_inputs(call, kw):
 ])
 def test_act_bwd_refuses_outputs_that_are_inputs(kw):
     assert bwd(pre=P, dout=2 * P, **kw) == L.MOE_EINVAL
+
+
+@pytest.mark.parametrize("kw", [
+    dict(act=1), dict(act=9), dict(act=0), dict(act=9, G=8),        # a batch without tokens: none of its tensors has an address
+    dict(act=9, G=8, db=P, acc=1, st=P, nv=P, ws=None, nws=0), dict(act=0, db=P, acc=1, ws=None, nws=0),
+])
+def test_act_bwd_of_no_rows(kw):
+    assert bwd(M=0, pre=None, dout=None, dpre=None, **kw) == L.MOE_OK

@@ -3,6 +3,7 @@ around it: on its own output, in shares, with batches of other sizes."""
 import pytest
 import torch
 
+from scatter_grouped_gemm_amd import _lib as L
 from epilogue_util import activation
 from gpu_util import DEV, announce
 from test_gpu_epilogue_layer import Case, check_grads, off
@@ -140,3 +141,36 @@ def experts_alone(c, q):
     out = out + activation(q["x"] @ q["s13"].t(), c.act) @ q["s2"].t()
     out.backward(c.dout.double())
     return q
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(router=False), dict(S=0), dict(bias=False), dict(router=False, S=0)])
+def test_training_on_a_batch_without_tokens(kw):
+    """A share of a batch may be empty: no gradient then, or (accumulate) the one before."""
+    announce("no tokens", kw)
+    c = Case(train=True, **kw)
+    give = () if c.gate is not None else (torch.randn(200, 16, device=DEV),)
+    c.layer(c.x, *give)
+    c.layer.backward(c.dout)
+    before = [g.clone() for g in c.layer.gradients()]
+    for accumulate in (True, False):
+        out = c.layer(c.x[:0], *(t[:0] for t in give))
+        dx, dlogits = c.layer.backward(c.dout[:0], accumulate=accumulate)
+        assert out.shape == dx.shape == (0, 256) and dlogits.shape == (0, 16)
+        for g, b in zip(c.layer.gradients(), before):
+            assert torch.equal(g, b) if accumulate else (g == 0).all()
+
+
+@pytest.mark.parametrize("act", ["none", "gelu", "swiglu_clamp"])
+@pytest.mark.parametrize("G", [1, 3])
+def test_bias_gradients_of_no_rows(act, G):
+    """Compact and dense layouts of no rows: 0, or what is there."""
+    N = 256
+    none = lambda n: torch.empty(0, n, dtype=BF, device=DEV)  # noqa: E731
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32, device=DEV)  # noqa: E731
+    kw = {} if G == 1 else dict(m_indices=i32(0), expert_start_loc=i32(G), num_valid=i32(G))
+    for dtype in (F32, BF):
+        db = torch.full((G, N), 3.0, dtype=dtype, device=DEV)
+        for accumulate, want in ((True, 3.0), (False, 0.0)):
+            L.moe_act_bwd(none(N), none(N // 2 if act == "swiglu_clamp" else N), none(N), act, dbias=db, accumulate=accumulate, **kw)
+            assert (db == want).all()
+    L.moe_act_bwd(none(N), none(N // 2 if act == "swiglu_clamp" else N), none(N), act, m_indices=kw.get("m_indices"))

@@ -26,9 +26,13 @@ int32_t act_args(int32_t dtype, const void* A, const uint8_t* A_scale, const voi
   if (out_dtype != MOE_DTYPE_BF16 && !(out_dtype == MOE_DTYPE_FP8_E4M3_UE8M0 && a.act.gated)) return MOE_EUNSUPPORTED;
   if (bias && bias_dtype != MOE_DTYPE_BF16 && bias_dtype != MOE_DTYPE_FP32) return MOE_EUNSUPPORTED;
   if (pre && dtype != MOE_DTYPE_BF16) return MOE_EUNSUPPORTED;
+  if (M == 0) {  // tensors without elements have no address
+    A = B;
+    out = const_cast<void*>(B);
+    A_scale = B_scale;
+  }
   const int32_t st = validate_gemm(dtype, A, A_scale, B, B_scale, out, N, K, G);
-  if (st != MOE_OK) return st;
-  if (M == 0) return MOE_OK;
+  if (st != MOE_OK || M == 0) return st;
   if (out == A || out == B || out == bias || (pre && (pre == A || pre == B || pre == out || pre == bias))) return MOE_EINVAL;
   if (!rowinfo || (out_dtype == MOE_DTYPE_FP8_E4M3_UE8M0 && !out_scale)) return MOE_EINVAL;
   if (!aligned16(A) || !aligned16(B) || !aligned16(bias) || !aligned16(out) || !aligned16(pre)) return MOE_EUNSUPPORTED;

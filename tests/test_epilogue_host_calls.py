@@ -34,3 +34,11 @@ def test_act_bwd_refuses_outputs_that_are_inputs(kw):
 ])
 def test_act_bwd_of_no_rows(kw):
     assert bwd(M=0, pre=None, dout=None, dpre=None, **kw) == L.MOE_OK
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(), L.MOE_OK), (dict(act=9), L.MOE_OK), (dict(dtype=1, Bs=P), L.MOE_OK), (dict(dtype=3, Bs=P, act=9, odt=1), L.MOE_OK),
+    (dict(B=None), L.MOE_EINVAL), (dict(N=64), L.MOE_EUNSUPPORTED), (dict(dtype=1), L.MOE_EUNSUPPORTED), (dict(act=6), L.MOE_EINVAL),
+])
+def test_contig_of_no_rows(kw, want):
+    assert contig(M=0, A=None, out=None, m=None, **kw) == want

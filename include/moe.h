@@ -411,8 +411,8 @@ int32_t moe_combine(const void* Y, int64_t num_rows, const int32_t* src2dst,
  * Products with an epilogue.  The product is summed in fp32 over ascending k (with
  * quantised weights the products of 128 of k by the matrix core, to about 2^-15 of the
  * largest, and these sums in fp32), and bias, activation and residual follow in fp32
- * before the one rounding to the output's type.  A row's result depends on its own row and its weights alone: it
- * is the same for any number of rows, and in both layouts.
+ * before the one rounding to the output's type.  A row's result depends on its own row
+ * and its weights alone: it is the same for any number of rows, and in both layouts.
  * ------------------------------------------------------------------------- */
 
 /* Dense product: with p[m][n] = sum over k of A[m][k] * B[n][k] + bias[n],
@@ -536,7 +536,8 @@ size_t moe_act_bwd_ws_bytes(int64_t M, int32_t N, int32_t G);
  *                 rounded once to its type
  * At a gate or up part that equals its limit the cut passes the gradient on, past
  * it the part's gradient is 0.
- * act' of a NaN is one; at the infinities it is its limit (0 and, but for RELU2, 1).
+ * act' of a NaN is a NaN; at the infinities it is its limit (0 below, 1 above, where
+ * RELU2's is infinite).
  *   Rows: m_indices (compact), masked_m with max_m (masked; M = G*max_m) or, both
  *   NULL, every row (then G = 1).  Other rows of dpre are left as they were and are
  *   part of no sum.
